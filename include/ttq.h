@@ -83,6 +83,7 @@ typedef struct {
 /* Sticky device error bits (read with ttq_device_error). */
 #define TTQ_DEVERR_TIMEOUT 0x1u    /* a bounded wait inside a kernel gave up */
 #define TTQ_DEVERR_FP16_RANGE 0x2u /* |x / s| exceeded the fp16 range        */
+#define TTQ_DEVERR_INDEX 0x4u      /* an adapter or expert index out of range */
 
 /* ---------------------------------------------------------------------
  * Packed code layout (TTQ review, Proposed method, bullet 1: group-wise
@@ -413,6 +414,128 @@ ttq_status ttq_lowrank_residual(const void* W, int64_t N, int64_t K,
                                 int64_t ldw, const void* B, const void* A,
                                 int r, void* R, int64_t ldr, void* stream);
 
+/* ---------------------------------------------------------------------
+ * Weights that a token selects. The pages describe one weight per layer;
+ * the calls below serve models and batches in which a token picks the
+ * weights it meets: the experts of a mixture-of-experts layer (packed as
+ * the projection's weights are) and the low-rank adapter of its request
+ * (beside one shared projection). Inference only, as the rest of the
+ * library.
+ * ------------------------------------------------------------------- */
+
+/* How a router scores its experts. */
+typedef enum { TTQ_SCORE_SOFTMAX = 0, TTQ_SCORE_SIGMOID = 1 } ttq_score;
+/* The gated activation of an expert: silu(v) = v / (1 + e^-v), or
+ * gelu_tanh(v) = v/2 (1 + tanh(sqrt(2/pi) (v + 0.044715 v^3))). */
+typedef enum { TTQ_ACT_SILU = 0, TTQ_ACT_GELU_TANH = 1 } ttq_act;
+
+/* The router of a mixture-of-experts layer: each token's top_k experts.
+ *   logit[t][e] = sum_j X[t][j] W[e][j]
+ *   score = softmax over the E experts, or sigmoid, of the logits
+ *   a token's experts are the top_k largest of score + bias (of the logits
+ *   for softmax without bias: the same order); equal values go to the lowest
+ *   expert, and a NaN ranks below every number. They are written in that
+ *   order:
+ *     ids[t][i] = expert, weights[t][i] = scaling * score
+ *   with the scores first divided by their sum over the token's top_k when
+ *   renormalize is 1 (a sum of 0 gives weights of 0).
+ *   X        [T, K] of dtype xt, row pitch ldx.
+ *   W        [E, K] of dtype wt, row pitch ldw.
+ *   bias     [E] float32, used for the choice only; NULL for none.
+ *   ids      [T, top_k] int32, dense; weights [T, top_k] float32, dense.
+ * X and W start on 16-byte boundaries and their rows are 16-byte aligned;
+ * K % 8 == 0, 1 <= E <= 512, 1 <= top_k <= min(E, 32), scaling finite.
+ * Products accumulate in fp32, the partial sums and the scores in fp64, so
+ * two experts are told apart down to about 1e-7 of the logits' size.
+ * Deterministic. */
+ttq_status ttq_moe_route(const void* X, ttq_dtype xt, int64_t T, int64_t K,
+                         int64_t ldx, const void* W, ttq_dtype wt, int64_t E,
+                         int64_t ldw, const float* bias, int top_k,
+                         ttq_score score, int renormalize, float scaling,
+                         int32_t* ids, float* weights, void* stream);
+
+/* A mixture-of-experts layer on packed low-bit experts, for a few tokens
+ * (T <= 64: a decode step). With x = X diag(inv_s), expert e's weights
+ * U_e [2I, K] (rows 0..I-1 the gate, I..2I-1 the other factor) and D_e
+ * [K, I] in the packed layout, and act the gated activation:
+ *   h[t][e]   = act(U_e[:I] x_t) * (U_e[I:] x_t)
+ *   Y[t]      = sum_i weights[t][i] D_e (h[t][e] * inv_s_mid[e]),
+ *                                                       e = ids[t][i]
+ *   X        [T, K] of dtype xt, row pitch ldx; inv_s [K] float32.
+ *   ids      [T, top_k] int32, dense. A negative id is no expert (padding):
+ *            it adds nothing. An id >= E adds nothing and raises
+ *            TTQ_DEVERR_INDEX. An id given twice for a token counts twice.
+ *   weights  [T, top_k] float32, dense.
+ *   up_codes, up_delta, up_zero        E stacked [2I, K] packed weights:
+ *            [E * 2I][ttq_codes_ld(K, bits)] and so on (one
+ *            ttq_quantize_rtn_grouped call on the stacked matrix).
+ *   inv_s_mid  [E, I] float32, dense.
+ *   down_codes, down_delta, down_zero  E stacked [K, I] packed weights.
+ *   Y        [T, K] of dtype yt, row pitch ldy. Every row is written; a
+ *            token without experts gets zeros.
+ *   workspace  ttq_moe_lowbit_workspace_size(T, K, I, top_k) bytes,
+ *            16-byte aligned, caller-owned; scratch, overwritten. Calls that
+ *            may overlap on the GPU need different workspaces.
+ * Codes are multiplied as exact integers and Delta is applied in fp32. The
+ * activations x and h inv_s_mid are scaled by a power of two per token and
+ * rounded once to fp16 for a bf16 Y, or held in two fp16 terms (22 bits) for
+ * an fp16 or fp32 Y; sums are fp32. Every expert's weights are read once
+ * (its tokens up to 32 at a time).
+ * Requires 1 <= T <= 64 (more: TTQ_ERR_UNSUPPORTED), 1 <= E <= 512,
+ * 1 <= top_k <= 32, K % 32 == 0, I % 32 == 0, K % group == 0,
+ * I % group == 0. Deterministic. */
+size_t ttq_moe_lowbit_workspace_size(int64_t T, int64_t K, int64_t I,
+                                     int top_k);
+ttq_status ttq_moe_lowbit(const void* X, ttq_dtype xt, int64_t T, int64_t K,
+                          int64_t ldx, const int32_t* ids,
+                          const float* weights, int top_k, int64_t E,
+                          const float* inv_s, const uint32_t* up_codes,
+                          const float* up_delta, const uint8_t* up_zero,
+                          int64_t I, const float* inv_s_mid,
+                          const uint32_t* down_codes, const float* down_delta,
+                          const uint8_t* down_zero, int bits, int group,
+                          ttq_act act, void* Y, ttq_dtype yt, int64_t ldy,
+                          void* workspace, size_t workspace_bytes,
+                          void* stream);
+
+/* Low-rank adapters of many requests beside one shared projection:
+ *   out[t] = Y[t] + scale[a] (X[t] A_a^T) B_a^T,   a = index[t]
+ * for the tokens with an adapter, out[t] = Y[t] (the same bits) for those
+ * without.
+ *
+ * ttq_adapters_plan groups a batch's tokens by adapter, once for all the
+ * projections of all the layers the batch runs through:
+ *   index  [T] int32: the token's adapter, negative for none. An index >= L
+ *          counts as none and raises TTQ_DEVERR_INDEX.
+ *   plan   int32 device buffer of ttq_adapters_plan_size(T, L) entries,
+ *          16-byte aligned. It depends on index alone and is only read by
+ *          ttq_adapters_add, so streams may share it.
+ *   1 <= T <= 2^20, 1 <= L <= 8192.
+ * ttq_adapters_add:
+ *   X      [T, K] of dtype xt, row pitch ldx. 16-byte aligned rows.
+ *   A      [L, r, K] and B [L, N, r] of dtype xt, dense, 16-byte aligned.
+ *          An adapter of a lower rank is padded with zeros.
+ *   scale  [L] float32, or NULL for 1.
+ *   Y      [T, N] of dtype yt, row pitch ldy; out [T, N] of dtype yt, row
+ *          pitch ldo. out may be Y itself (ldo == ldy: rows without an
+ *          adapter are then left untouched), but may not overlap Y otherwise,
+ *          nor X, A, B or plan.
+ * T and L are the plan's. K % 8 == 0, 1 <= r <= 64, r % 4 == 0.
+ * Products of 16-bit values accumulate in fp32; fp32 values are split into
+ * three bf16 terms (24 bits); X A^T is kept in fp32 and enters the second
+ * product in two 16-bit terms (three bf16 terms for fp32). Y is rounded
+ * once. Deterministic. */
+int64_t ttq_adapters_plan_size(int64_t T, int64_t L);
+ttq_status ttq_adapters_plan(const int32_t* index, int64_t T, int64_t L,
+                             int32_t* plan, int64_t plan_entries,
+                             void* stream);
+ttq_status ttq_adapters_add(const void* X, ttq_dtype xt, int64_t T, int64_t K,
+                            int64_t ldx, const void* A, const void* B,
+                            const float* scale, int64_t L, int r, int64_t N,
+                            const int32_t* plan, int64_t plan_entries,
+                            const void* Y, ttq_dtype yt, int64_t ldy,
+                            void* out, int64_t ldo, void* stream);
+
 /* Expand packed codes to one uint8 per weight: q_out [N][K] (device).
  * Inverse of the packing in ttq_quantize_rtn_grouped. */
 ttq_status ttq_unpack_codes(const uint32_t* codes, int64_t N, int64_t K,
@@ -443,7 +566,9 @@ ttq_status ttq_selftest_bounded_wait(int arrive, uint32_t* out, void* stream);
  * ttq_awq_scales_sharded added; 6: ttq_projection_stats_rows,
  * ttq_w_lowbit_gemm_prepared_stats and ttq_stats_reduce added; 7:
  * ttq_quantize_gemm_prepared added; 8: ttq_lowrank_factors,
- * ttq_lowrank_factors_workspace_size and ttq_lowrank_residual added). */
+ * ttq_lowrank_factors_workspace_size and ttq_lowrank_residual added). The
+ * calls on weights that a token selects (ttq_moe_*, ttq_adapters_*) were
+ * added within 8: they change no call that was there. */
 int ttq_abi_version(void);
 
 #ifdef __cplusplus

@@ -419,6 +419,173 @@ TTQ_EXPORT ttq_status ttq_lowrank_residual(const void* W, int64_t N, int64_t K,
                                  as_stream(stream));
 }
 
+TTQ_EXPORT ttq_status ttq_moe_route(const void* X, ttq_dtype xt, int64_t T,
+                                    int64_t K, int64_t ldx, const void* W,
+                                    ttq_dtype wt, int64_t E, int64_t ldw,
+                                    const float* bias, int top_k,
+                                    ttq_score score, int renormalize,
+                                    float scaling, int32_t* ids,
+                                    float* weights, void* stream) {
+  if (!X || !W || !ids || !weights || !valid_dtype(xt) || !valid_dtype(wt) ||
+      T < 1 || T >= ((int64_t)1 << 31) || K < 8 || K % 8 != 0 ||
+      K > (1 << 20) || E < 1 || E > 512 || top_k < 1 || top_k > 32 ||
+      top_k > E || ldx < K || ldw < K || !rows_aligned(X, xt, ldx) ||
+      !rows_aligned(W, wt, ldw) || (bias && !aligned(bias, 4)) ||
+      (score != TTQ_SCORE_SOFTMAX && score != TTQ_SCORE_SIGMOID) ||
+      (renormalize != 0 && renormalize != 1) || !isfinite(scaling) ||
+      !aligned(ids, 4) || !aligned(weights, 4))
+    return TTQ_ERR_INVALID_ARG;
+  const size_t nb = (size_t)T * top_k * 4,
+               nx = (size_t)((T - 1) * ldx + K) * dtype_bytes(xt),
+               nw = (size_t)((E - 1) * ldw + K) * dtype_bytes(wt);
+  if (overlaps(ids, nb, weights, nb) || overlaps(ids, nb, X, nx) ||
+      overlaps(weights, nb, X, nx) || overlaps(ids, nb, W, nw) ||
+      overlaps(weights, nb, W, nw))
+    return TTQ_ERR_INVALID_ARG;
+  return launch_moe_route(X, xt, T, K, ldx, W, wt, E, ldw, bias, top_k, score,
+                          renormalize, scaling, ids, weights,
+                          as_stream(stream));
+}
+
+TTQ_EXPORT size_t ttq_moe_lowbit_workspace_size(int64_t T, int64_t K,
+                                                int64_t I, int top_k) {
+  if (T < 1 || T > 64 || K < 32 || K % 32 != 0 || K > (1 << 20) || I < 32 ||
+      I % 32 != 0 || I > (1 << 20) || top_k < 1 || top_k > 32)
+    return 0;
+  return moe_workspace_bytes(T, K, I, top_k);
+}
+
+TTQ_EXPORT ttq_status ttq_moe_lowbit(
+    const void* X, ttq_dtype xt, int64_t T, int64_t K, int64_t ldx,
+    const int32_t* ids, const float* weights, int top_k, int64_t E,
+    const float* inv_s, const uint32_t* up_codes, const float* up_delta,
+    const uint8_t* up_zero, int64_t I, const float* inv_s_mid,
+    const uint32_t* down_codes, const float* down_delta,
+    const uint8_t* down_zero, int bits, int group, ttq_act act, void* Y,
+    ttq_dtype yt, int64_t ldy, void* workspace, size_t workspace_bytes,
+    void* stream) {
+  if (!X || !ids || !weights || !inv_s || !up_codes || !up_delta || !up_zero ||
+      !inv_s_mid || !down_codes || !down_delta || !down_zero || !Y ||
+      !workspace || !valid_dtype(xt) || !valid_dtype(yt) || T < 1 || K < 32 ||
+      K % 32 != 0 || K > (1 << 20) || I < 32 || I % 32 != 0 ||
+      I > (1 << 20) || E < 1 || E > 512 || top_k < 1 || top_k > 32 ||
+      bits < 2 || bits > 8 || !valid_group(group) || K % group != 0 ||
+      I % group != 0 || (act != TTQ_ACT_SILU && act != TTQ_ACT_GELU_TANH) ||
+      ldx < K || ldy < K || !rows_aligned(X, xt, ldx) ||
+      !aligned(Y, dtype_bytes(yt)) || !aligned(ids, 4) ||
+      !aligned(weights, 4) || !aligned(inv_s, 16) || !aligned(inv_s_mid, 4) ||
+      !aligned(up_codes, 16) || !aligned(up_delta, 16) ||
+      !aligned(up_zero, 16) || !aligned(down_codes, 16) ||
+      !aligned(down_delta, 16) || !aligned(down_zero, 16) ||
+      !aligned(workspace, 16))
+    return TTQ_ERR_INVALID_ARG;
+  if (T > 64) return TTQ_ERR_UNSUPPORTED;
+  if (workspace_bytes < moe_workspace_bytes(T, K, I, top_k))
+    return TTQ_ERR_INVALID_ARG;
+  const size_t nx = (size_t)((T - 1) * ldx + K) * dtype_bytes(xt),
+               ny = (size_t)((T - 1) * ldy + K) * dtype_bytes(yt),
+               ns = (size_t)T * top_k * 4;
+  if (overlaps(workspace, workspace_bytes, X, nx) ||
+      overlaps(workspace, workspace_bytes, Y, ny) ||
+      overlaps(workspace, workspace_bytes, ids, ns) ||
+      overlaps(workspace, workspace_bytes, weights, ns) ||
+      overlaps(Y, ny, ids, ns) || overlaps(Y, ny, weights, ns))
+    return TTQ_ERR_INVALID_ARG;
+  MoeArgs a;
+  a.X = X;
+  a.xt = xt;
+  a.T = T;
+  a.K = K;
+  a.ldx = ldx;
+  a.ids = ids;
+  a.weights = weights;
+  a.top_k = top_k;
+  a.E = E;
+  a.inv_s = inv_s;
+  a.up_codes = up_codes;
+  a.up_delta = up_delta;
+  a.up_zero = up_zero;
+  a.I = I;
+  a.inv_s_mid = inv_s_mid;
+  a.down_codes = down_codes;
+  a.down_delta = down_delta;
+  a.down_zero = down_zero;
+  a.bits = bits;
+  a.group = group;
+  a.act = act;
+  a.Y = Y;
+  a.yt = yt;
+  a.ldy = ldy;
+  a.workspace = workspace;
+  return launch_moe_lowbit(a, as_stream(stream));
+}
+
+namespace {
+bool plan_sizes(int64_t T, int64_t L) {
+  return T >= 1 && T <= (1 << 20) && L >= 1 && L <= 8192;
+}
+}  // namespace
+
+TTQ_EXPORT int64_t ttq_adapters_plan_size(int64_t T, int64_t L) {
+  return plan_sizes(T, L) ? adapters_plan_entries(T, L) : 0;
+}
+
+TTQ_EXPORT ttq_status ttq_adapters_plan(const int32_t* index, int64_t T,
+                                        int64_t L, int32_t* plan,
+                                        int64_t plan_entries, void* stream) {
+  if (!index || !plan || !plan_sizes(T, L) || !aligned(index, 4) ||
+      !aligned(plan, 16) || plan_entries < adapters_plan_entries(T, L) ||
+      overlaps(index, (size_t)T * 4, plan, (size_t)plan_entries * 4))
+    return TTQ_ERR_INVALID_ARG;
+  return launch_adapters_plan(index, T, L, plan, as_stream(stream));
+}
+
+TTQ_EXPORT ttq_status ttq_adapters_add(
+    const void* X, ttq_dtype xt, int64_t T, int64_t K, int64_t ldx,
+    const void* A, const void* B, const float* scale, int64_t L, int r,
+    int64_t N, const int32_t* plan, int64_t plan_entries, const void* Y,
+    ttq_dtype yt, int64_t ldy, void* out, int64_t ldo, void* stream) {
+  if (!X || !A || !B || !plan || !Y || !out || !valid_dtype(xt) ||
+      !valid_dtype(yt) || !plan_sizes(T, L) || K < 8 || K % 8 != 0 ||
+      K > (1 << 20) || N < 1 || N > (1 << 20) || r < 1 || r > 64 ||
+      r % 4 != 0 || ldx < K || ldy < N || ldo < N ||
+      !rows_aligned(X, xt, ldx) || !aligned(A, 16) || !aligned(B, 16) ||
+      !aligned(plan, 16) || (scale && !aligned(scale, 4)) ||
+      !aligned(Y, dtype_bytes(yt)) || !aligned(out, dtype_bytes(yt)) ||
+      plan_entries < adapters_plan_entries(T, L))
+    return TTQ_ERR_INVALID_ARG;
+  const size_t eb = dtype_bytes(xt), yb = dtype_bytes(yt);
+  const size_t nx = (size_t)((T - 1) * ldx + K) * eb,
+               ny = (size_t)((T - 1) * ldy + N) * yb,
+               no = (size_t)((T - 1) * ldo + N) * yb,
+               na = (size_t)L * r * K * eb, nb = (size_t)L * r * N * eb;
+  const bool in_place = out == Y && ldo == ldy;
+  if ((!in_place && overlaps(out, no, Y, ny)) || overlaps(out, no, X, nx) ||
+      overlaps(out, no, A, na) || overlaps(out, no, B, nb) ||
+      overlaps(out, no, plan, (size_t)plan_entries * 4) ||
+      (scale && overlaps(out, no, scale, (size_t)L * 4)))
+    return TTQ_ERR_INVALID_ARG;
+  AdapterArgs g;
+  g.X = X;
+  g.xt = xt;
+  g.T = T;
+  g.K = K;
+  g.ldx = ldx;
+  g.A = A;
+  g.B = B;
+  g.scale = scale;
+  g.L = L;
+  g.r = r;
+  g.N = N;
+  g.plan = plan;
+  g.Y = Y;
+  g.yt = yt;
+  g.ldy = ldy;
+  g.out = out;
+  g.ldo = ldo;
+  return launch_adapters_add(g, as_stream(stream));
+}
+
 TTQ_EXPORT ttq_status ttq_unpack_codes(const uint32_t* codes, int64_t N,
                                        int64_t K, int bits, uint8_t* q_out,
                                        void* stream) {

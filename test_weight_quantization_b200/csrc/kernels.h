@@ -119,4 +119,64 @@ ttq_status launch_lowrank_residual(const void* W, int64_t N, int64_t K,
                                    int r, void* R, int64_t ldr,
                                    cudaStream_t st);
 
+// The router of a mixture-of-experts layer (route.cu).
+ttq_status launch_moe_route(const void* X, ttq_dtype xt, int64_t T, int64_t K,
+                            int64_t ldx, const void* W, ttq_dtype wt,
+                            int64_t E, int64_t ldw, const float* bias,
+                            int top_k, int score, int renormalize,
+                            float scaling, int32_t* ids, float* weights,
+                            cudaStream_t st);
+
+// A mixture-of-experts layer on packed experts (moe.cu); the fields are the
+// arguments of ttq_moe_lowbit.
+struct MoeArgs {
+  const void* X;
+  ttq_dtype xt;
+  int64_t T, K, ldx;
+  const int32_t* ids;
+  const float* weights;
+  int top_k;
+  int64_t E;
+  const float* inv_s;
+  const uint32_t* up_codes;
+  const float* up_delta;
+  const uint8_t* up_zero;
+  int64_t I;
+  const float* inv_s_mid;
+  const uint32_t* down_codes;
+  const float* down_delta;
+  const uint8_t* down_zero;
+  int bits, group;
+  ttq_act act;
+  void* Y;
+  ttq_dtype yt;
+  int64_t ldy;
+  void* workspace;
+};
+size_t moe_workspace_bytes(int64_t T, int64_t K, int64_t I, int top_k);
+ttq_status launch_moe_lowbit(const MoeArgs& a, cudaStream_t st);
+
+// Low-rank adapters of many requests (adapters.cu); the fields are the
+// arguments of ttq_adapters_add.
+struct AdapterArgs {
+  const void* X;
+  ttq_dtype xt;
+  int64_t T, K, ldx;
+  const void *A, *B;
+  const float* scale;
+  int64_t L;
+  int r;
+  int64_t N;
+  const int32_t* plan;
+  const void* Y;
+  ttq_dtype yt;
+  int64_t ldy;
+  void* out;
+  int64_t ldo;
+};
+int64_t adapters_plan_entries(int64_t T, int64_t L);
+ttq_status launch_adapters_plan(const int32_t* index, int64_t T, int64_t L,
+                                int32_t* plan, cudaStream_t st);
+ttq_status launch_adapters_add(const AdapterArgs& a, cudaStream_t st);
+
 }  // namespace ttq

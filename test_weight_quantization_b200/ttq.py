@@ -24,6 +24,7 @@ _LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)),
 TTQ_OK = 0
 DEVERR_TIMEOUT = 0x1
 DEVERR_FP16_RANGE = 0x2
+DEVERR_INDEX = 0x4
 
 _DTYPE = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
 
@@ -72,6 +73,15 @@ def _load() -> ctypes.CDLL:
         "ttq_lowrank_factors_workspace_size": [I64, I64, I],
         "ttq_lowrank_factors": [P, I64, I64, I64, P, P, I, I, P, P, P, SZ, P],
         "ttq_lowrank_residual": [P, I64, I64, I64, P, P, I, P, I64, P],
+        "ttq_moe_route": [P, I, I64, I64, I64, P, I, I64, I64, P, I, I, I, F,
+                          P, P, P],
+        "ttq_moe_lowbit_workspace_size": [I64, I64, I64, I],
+        "ttq_moe_lowbit": [P, I, I64, I64, I64, P, P, I, I64, P, P, P, P, I64,
+                           P, P, P, P, I, I, I, P, I, I64, P, SZ, P],
+        "ttq_adapters_plan_size": [I64, I64],
+        "ttq_adapters_plan": [P, I64, I64, P, I64, P],
+        "ttq_adapters_add": [P, I, I64, I64, I64, P, P, P, I64, I, I64, P,
+                             I64, P, I, I64, P, I64, P],
     }
     for name, args in sig.items():
         fn = getattr(lib, name)
@@ -83,6 +93,8 @@ def _load() -> ctypes.CDLL:
     lib.ttq_groups_ld.restype = I64
     lib.ttq_projection_stats_rows.restype = I64
     lib.ttq_lowrank_factors_workspace_size.restype = SZ
+    lib.ttq_moe_lowbit_workspace_size.restype = SZ
+    lib.ttq_adapters_plan_size.restype = I64
     return lib
 
 
@@ -100,7 +112,9 @@ EXPORTS = ("ttq_act_stats", "ttq_awq_scales", "ttq_act_stats_scales",
            "ttq_projection_stats_rows", "ttq_w_lowbit_gemm_prepared_stats",
            "ttq_stats_reduce", "ttq_quantize_gemm_prepared",
            "ttq_lowrank_factors_workspace_size", "ttq_lowrank_factors",
-           "ttq_lowrank_residual")
+           "ttq_lowrank_residual", "ttq_moe_route",
+           "ttq_moe_lowbit_workspace_size", "ttq_moe_lowbit",
+           "ttq_adapters_plan_size", "ttq_adapters_plan", "ttq_adapters_add")
 
 
 class _Params(ctypes.Structure):
@@ -654,6 +668,150 @@ def lowrank_residual(W: torch.Tensor, B: torch.Tensor, A: torch.Tensor,
     _check(_lib.ttq_lowrank_residual(W.data_ptr(), N, K, ldw, B.data_ptr(),
                                      A.data_ptr(), r, out.data_ptr(), ldr,
                                      _stream()), "ttq_lowrank_residual")
+    return out
+
+
+_SCORE = {"softmax": 0, "sigmoid": 1}
+_ACT = {"silu": 0, "gelu": 1}
+
+
+def _named(table: dict, value, name: str) -> int:
+    if value not in table:
+        raise TTQError(f"{name} must be one of {', '.join(table)}, not "
+                       f"{value!r}")
+    return table[value]
+
+
+def moe_route(X: torch.Tensor, W: torch.Tensor, top_k: int,
+              bias: torch.Tensor | None = None, score: str = "softmax",
+              renormalize: bool = True, scaling: float = 1.0,
+              ids: torch.Tensor | None = None,
+              weights: torch.Tensor | None = None):
+    """Each token's top_k experts of the router W [E, K]: (ids int32, weights
+    fp32), both [T, top_k], the best expert first. ``score`` is "softmax" or
+    "sigmoid"; ``bias`` [E] fp32 takes part in the choice only."""
+    ldx, ldw = _rows(X, "X"), _rows(W, "W")
+    T, K = X.shape
+    E = W.shape[0]
+    if W.shape[1] != K:
+        raise TTQError(f"W must have {K} columns, got {W.shape[1]}")
+    if bias is not None:
+        _buf(bias, "bias", torch.float32, E)
+    if ids is None:
+        ids = torch.empty((T, top_k), dtype=torch.int32, device=X.device)
+    if weights is None:
+        weights = torch.empty((T, top_k), dtype=torch.float32,
+                              device=X.device)
+    _buf(ids, "ids", torch.int32, T, top_k)
+    _buf(weights, "weights", torch.float32, T, top_k)
+    _check(_lib.ttq_moe_route(
+        X.data_ptr(), _code(X, "X"), T, K, ldx, W.data_ptr(), _code(W, "W"),
+        E, ldw, _ptr(bias), int(top_k), _named(_SCORE, score, "score"),
+        1 if renormalize else 0, float(scaling), ids.data_ptr(),
+        weights.data_ptr(), _stream()), "ttq_moe_route")
+    return ids, weights
+
+
+def moe_lowbit_workspace_size(T: int, K: int, I: int, top_k: int) -> int:
+    return int(_lib.ttq_moe_lowbit_workspace_size(T, K, I, top_k))
+
+
+def moe_lowbit(X: torch.Tensor, ids: torch.Tensor, weights: torch.Tensor,
+               inv_s: torch.Tensor, up, inv_s_mid: torch.Tensor, down,
+               bits: int, group: int, act: str = "silu",
+               out: torch.Tensor | None = None, out_dtype=None,
+               workspace: torch.Tensor | None = None) -> torch.Tensor:
+    """A mixture-of-experts layer on packed experts for up to 64 tokens:
+    Y[t] = sum_i weights[t, i] D_e (act(G_e x) * (U_e x) * inv_s_mid[e]),
+    e = ids[t, i], x = X[t] * inv_s. ``up`` is (codes, delta, zero) of the E
+    stacked [2I, K] weights (gate rows first), ``down`` of the E stacked
+    [K, I] weights, both from quantize_rtn_grouped; inv_s_mid is [E, I]
+    fp32. A negative id is no expert. ``act`` is "silu" or "gelu" (tanh)."""
+    ldx = _rows(X, "X")
+    T, K = X.shape
+    _dev(inv_s_mid, "inv_s_mid")
+    if inv_s_mid.dim() != 2:
+        raise TTQError("inv_s_mid must be [E, I]")
+    E, I = inv_s_mid.shape
+    _buf(inv_s_mid, "inv_s_mid", torch.float32, E, I)
+    _dev(ids, "ids")
+    if ids.dim() != 2:
+        raise TTQError("ids must be [T, top_k]")
+    top_k = ids.shape[1]
+    _buf(ids, "ids", torch.int32, T, top_k)
+    _buf(weights, "weights", torch.float32, T, top_k)
+    _buf(inv_s, "inv_s", torch.float32, K)
+    _packed(*up, E * 2 * I, K, bits, group)
+    _packed(*down, E * K, I, bits, group)
+    if out is None:
+        out = torch.empty((T, K), dtype=out_dtype or X.dtype, device=X.device)
+    ldy = _out(out, "out", T, K)
+    need = moe_lowbit_workspace_size(T, K, I, top_k)
+    if workspace is None:
+        workspace = torch.empty(max(need, 16), dtype=torch.uint8,
+                                device=X.device)
+    _buf(workspace, "workspace", torch.uint8, need)
+    _check(_lib.ttq_moe_lowbit(
+        X.data_ptr(), _code(X, "X"), T, K, ldx, ids.data_ptr(),
+        weights.data_ptr(), top_k, E, inv_s.data_ptr(), up[0].data_ptr(),
+        up[1].data_ptr(), up[2].data_ptr(), I, inv_s_mid.data_ptr(),
+        down[0].data_ptr(), down[1].data_ptr(), down[2].data_ptr(), bits,
+        group, _named(_ACT, act, "act"), out.data_ptr(), _code(out, "out"),
+        ldy, workspace.data_ptr(), workspace.numel(), _stream()),
+        "ttq_moe_lowbit")
+    return out
+
+
+def adapters_plan(index: torch.Tensor, L: int,
+                  plan: torch.Tensor | None = None) -> torch.Tensor:
+    """Groups a batch's tokens by adapter: ``index`` [T] int32 is each
+    token's adapter of L, negative for none. The plan (int32) serves every
+    adapters_add of the batch."""
+    _buf(index, "index", torch.int32, 0)
+    T = index.shape[0]
+    need = int(_lib.ttq_adapters_plan_size(T, int(L)))
+    if need <= 0:
+        raise TTQError(f"no adapter plan for T={T}, L={L}")
+    if plan is None:
+        plan = torch.empty(need, dtype=torch.int32, device=index.device)
+    _buf(plan, "plan", torch.int32, need)
+    _check(_lib.ttq_adapters_plan(index.data_ptr(), T, int(L),
+                                  plan.data_ptr(), plan.numel(), _stream()),
+           "ttq_adapters_plan")
+    return plan
+
+
+def adapters_add(X: torch.Tensor, A: torch.Tensor, B: torch.Tensor,
+                 plan: torch.Tensor, Y: torch.Tensor,
+                 scale: torch.Tensor | None = None,
+                 out: torch.Tensor | None = None) -> torch.Tensor:
+    """Y + scale[a] (X A_a^T) B_a^T of each token's adapter a, in place unless
+    ``out`` is given. A [L, r, K], B [L, N, r], scale [L] fp32; ``plan`` from
+    adapters_plan for this batch and L."""
+    ldx = _rows(X, "X")
+    T, K = X.shape
+    for t, name in ((A, "A"), (B, "B")):
+        _dev(t, name)
+        if t.dim() != 3 or not t.is_contiguous() or t.dtype != X.dtype:
+            raise TTQError(f"{name} must be a dense 3D {X.dtype} tensor")
+    L, r, N = A.shape[0], A.shape[1], B.shape[1]
+    if tuple(A.shape) != (L, r, K) or tuple(B.shape) != (L, N, r):
+        raise TTQError(f"A must be [L, r, {K}] and B [L, N, r], got "
+                       f"{tuple(A.shape)} and {tuple(B.shape)}")
+    if scale is not None:
+        _buf(scale, "scale", torch.float32, L)
+    ldy = _out(Y, "Y", T, N)
+    out = Y if out is None else out
+    ldo = _out(out, "out", T, N)
+    if out.dtype != Y.dtype:
+        raise TTQError(f"out must be {Y.dtype}, got {out.dtype}")
+    need = int(_lib.ttq_adapters_plan_size(T, L))
+    _buf(plan, "plan", torch.int32, max(need, 1))
+    _check(_lib.ttq_adapters_add(
+        X.data_ptr(), _code(X, "X"), T, K, ldx, A.data_ptr(), B.data_ptr(),
+        _ptr(scale), L, r, N, plan.data_ptr(), plan.numel(), Y.data_ptr(),
+        _code(Y, "Y"), ldy, out.data_ptr(), ldo, _stream()),
+        "ttq_adapters_add")
     return out
 
 
