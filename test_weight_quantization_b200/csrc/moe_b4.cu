@@ -1,0 +1,9 @@
+// moe_b4.cu — the expert kernels of ttq_moe_lowbit for 4-bit codes.
+#include "moe_tile.cuh"
+
+namespace ttq {
+namespace moe {
+template ttq_status launch_bits<4>(const UpArgs&, const DownArgs&,
+                                    cudaStream_t);
+}  // namespace moe
+}  // namespace ttq

@@ -1,0 +1,9 @@
+// moe_b8.cu — the expert kernels of ttq_moe_lowbit for 8-bit codes.
+#include "moe_tile.cuh"
+
+namespace ttq {
+namespace moe {
+template ttq_status launch_bits<8>(const UpArgs&, const DownArgs&,
+                                    cudaStream_t);
+}  // namespace moe
+}  // namespace ttq
