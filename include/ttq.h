@@ -480,8 +480,9 @@ ttq_status ttq_moe_route(const void* X, ttq_dtype xt, int64_t T, int64_t K,
  * activations x and h inv_s_mid are scaled by a power of two per token and
  * rounded once to fp16 for a bf16 Y, or held in two fp16 terms (22 bits) for
  * an fp16 or fp32 Y; sums are fp32. Every expert's weights are read once
- * (its tokens up to 32 at a time).
- * Requires 1 <= T <= 64 (more: TTQ_ERR_UNSUPPORTED), 1 <= E <= 512,
+ * (its tokens up to 16 at a time).
+ * Requires 1 <= T <= 64 and an expert whose packed matrices stay below 2^31
+ * bytes each (otherwise TTQ_ERR_UNSUPPORTED), 1 <= E <= 512,
  * 1 <= top_k <= 32, K % 32 == 0, I % 32 == 0, K % group == 0,
  * I % group == 0. Deterministic. */
 size_t ttq_moe_lowbit_workspace_size(int64_t T, int64_t K, int64_t I,

@@ -479,7 +479,12 @@ TTQ_EXPORT ttq_status ttq_moe_lowbit(
       !aligned(down_delta, 16) || !aligned(down_zero, 16) ||
       !aligned(workspace, 16))
     return TTQ_ERR_INVALID_ARG;
-  if (T > 64) return TTQ_ERR_UNSUPPORTED;
+  // an expert's packed matrix is addressed with 31-bit byte offsets
+  if (T > 64 || (2 * I + 32) * codes_ld(K, bits) * 4 >= ((int64_t)1 << 31) ||
+      (K + 32) * codes_ld(I, bits) * 4 >= ((int64_t)1 << 31) ||
+      (2 * I + 32) * groups_ld(K, group) * 4 >= ((int64_t)1 << 31) ||
+      (K + 32) * groups_ld(I, group) * 4 >= ((int64_t)1 << 31))
+    return TTQ_ERR_UNSUPPORTED;
   if (workspace_bytes < moe_workspace_bytes(T, K, I, top_k))
     return TTQ_ERR_INVALID_ARG;
   const size_t nx = (size_t)((T - 1) * ldx + K) * dtype_bytes(xt),

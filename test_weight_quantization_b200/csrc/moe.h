@@ -12,29 +12,66 @@ namespace ttq {
 namespace moe {
 
 constexpr int kMaxExperts = 512;
-constexpr int kMaxCols = 32;  // columns of an entry: 4 MMA tiles of 8
+constexpr int kMaxCols = 16;  // columns of an entry: 2 MMA tiles of 8
 
-// xhat: fp16 terms of x 2^k, [term][T][K], in the order the code pairs want;
-// xmax: bits of a token's largest |x|; h [T top_k][I] fp32 and hmax likewise.
+// The bit of an fp16 at which the code pairs of a lane's block enter the MMA
+// (pair i), and the largest of them. A pair is used where the unpacking finds
+// it if it ends below bit 10 there, otherwise it is shifted down; the
+// activations that meet pair i are stored with 2^(kMost - at(i)).
+template <int BITS, bool G16>
+struct Positions {
+  static constexpr int kMost = BITS == 2 ? (G16 ? 2 : 6)
+                               : BITS == 3 ? (G16 ? 3 : 6)
+                               : BITS <= 5 ? BITS
+                                           : 0;
+  static __host__ __device__ constexpr int at(int i) {
+    if (BITS >= 6) return 0;
+    if (G16 || BITS == 5) return i & 1 ? BITS : 0;
+    if (BITS == 2) return 2 * i;
+    if (BITS == 3) return i < 3 ? 3 * i : 6;
+    return i & 1 ? 4 : 0;
+  }
+};
+inline int position(int bits, bool g16, int i) {
+  switch (bits) {
+    case 2: return g16 ? Positions<2, true>::at(i) : Positions<2, false>::at(i);
+    case 3: return g16 ? Positions<3, true>::at(i) : Positions<3, false>::at(i);
+    case 4: return g16 ? Positions<4, true>::at(i) : Positions<4, false>::at(i);
+    case 5: return g16 ? Positions<5, true>::at(i) : Positions<5, false>::at(i);
+  }
+  return 0;
+}
+
+// k of the power of two that a row of activations carries: its largest value
+// (its bits) times 2^k 2^most lies in [2^13, 2^14).
+__host__ __device__ inline int row_exponent(uint32_t max_bits, int most) {
+  const int e = (int)(max_bits >> 23) - 127;
+  const int k = 13 - most - e;
+  return k < 126 ? k : 126;
+}
+
+// xhat: fp16 terms of the rows, [term][T][K], in the order the code pairs
+// want; xmax: bits of a token's largest |x|; h [T top_k][I] fp32, and hhat,
+// hmax as xhat and xmax for its rows.
 struct UpArgs {
-  const __half* xhat;
+  const uint4* xhat;
   const uint32_t* xmax;
   const int32_t* ids;
-  int T, K, I, E, top_k, group, act;
+  int T, K, I, E, top_k, group, act, rs;
   const uint32_t* codes;
   const float* delta;
   const uint8_t* zero;
   const float* inv_s_mid;
   float* h;
-  uint32_t* hmax;
+  ttq_dtype yt;
   uint32_t* err;
 };
 struct DownArgs {
-  const float* h;
+  const uint4* hhat;
   const uint32_t* hmax;
   const int32_t* ids;
   const float* weights;
-  int T, K, I, E, top_k, group;
+  int T, K, I, E, top_k, group, rs;
   const uint32_t* codes;
   const float* delta;
   const uint8_t* zero;
@@ -43,8 +80,8 @@ struct DownArgs {
   int64_t ldy;
 };
 
-template <int BITS>
-ttq_status launch_bits(const UpArgs& u, const DownArgs& d, cudaStream_t st);
+template <int BITS, typename Args>
+ttq_status launch_bits(const Args& a, cudaStream_t st);
 
 }  // namespace moe
 }  // namespace ttq

@@ -3,7 +3,7 @@
 
 namespace ttq {
 namespace moe {
-template ttq_status launch_bits<4>(const UpArgs&, const DownArgs&,
-                                    cudaStream_t);
+template ttq_status launch_bits<4, UpArgs>(const UpArgs&, cudaStream_t);
+template ttq_status launch_bits<4, DownArgs>(const DownArgs&, cudaStream_t);
 }  // namespace moe
 }  // namespace ttq

@@ -3,7 +3,7 @@
 
 namespace ttq {
 namespace moe {
-template ttq_status launch_bits<6>(const UpArgs&, const DownArgs&,
-                                    cudaStream_t);
+template ttq_status launch_bits<6, UpArgs>(const UpArgs&, cudaStream_t);
+template ttq_status launch_bits<6, DownArgs>(const DownArgs&, cudaStream_t);
 }  // namespace moe
 }  // namespace ttq

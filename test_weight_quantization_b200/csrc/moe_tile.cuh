@@ -4,24 +4,25 @@
 // An expert meets a handful of tokens per step, so its packed weights are
 // read once from HBM and used for a few products each: the kernels are bound
 // by those bytes, and by the instructions that unpack them. Per warp:
-//   - mma.sync m16n8k16 with 16 weight rows as M, up to 32 tokens as N (1, 2
-//     or 4 tiles of 8). tcgen05 would want 128 rows per tile and the weights
+//   - mma.sync m16n8k16 with 16 weight rows as M, up to 16 tokens as N (1 or 2
+//     tiles of 8). tcgen05 would want 128 rows per tile and the weights
 //     copied to TMEM or shared memory after unpacking; here an unpacked code
 //     pair goes from the register it was masked in straight into the MMA.
-//   - A code q enters as the fp16 bit pattern q << kAt, the subnormal
-//     q 2^(kAt-24): the mask that isolates two codes is all the conversion
-//     there is. Per group,
+//   - A code q enters as an fp16 bit pattern, the subnormal q 2^(P-24) for a
+//     code at bit P: one AND isolates two codes and is all the conversion
+//     there is. Codes are used at several P without a shift; the activations
+//     that meet them carry 2^(Pmax-P) (Positions). Per group,
 //       acc += D (sum q x - z sum x),
-//     with sum x from one more MMA whose A is all ones, in the same
-//     accumulator layout. D (fp32) and z are applied in fp32; 2^(24-kAt) and
+//     with sum x from one more MMA whose A undoes 2^(Pmax-P), in the same
+//     accumulator layout. D (fp32) and z are applied in fp32; 2^(24-Pmax) and
 //     the row's power of two return in the epilogue.
 //   - The contraction order inside a 32-code block is free as long as both
 //     operands agree: lane t of a quad owns codes 8t..8t+7 (for groups of 16:
 //     4t..4t+3 of both halves), which are consecutive bits of one word (4
 //     bits) or of two or three, and the activations are stored in that order.
 //   - Codes, delta and zero of 32 rows x 128 channels arrive by cp.async in a
-//     ring of stages of the warp's own; warps split the contraction and never
-//     wait for one another inside it.
+//     ring of stages of the warp's own; warps never wait for one another
+//     inside the contraction.
 #pragma once
 
 #include <cuda_fp16.h>
@@ -193,53 +194,93 @@ __device__ __forceinline__ void cp_async_ca(uint32_t dst, const void* src) {
                : "memory");
 }
 
-// The packed matrix of one layer half: stacked rows of `width` channels.
+// The packed matrices of one side of the experts, rows of 32 `blocks`
+// channels.
 struct Packed {
   const uint32_t* codes;
   const float* delta;
   const uint8_t* zero;
-  int64_t ldc, ldg;   // words, entries
-  int blocks;         // width / 32
+  int ldc, ldg;   // words, entries
+  int blocks;
   int group;
 };
 
-// Issues the copies of 32 rows (row r of the tile is matrix row base + r for
-// r < 16, base2 + r - 16 for the rest) x channels 128 c .. 128 c + 127.
+// A lane's share of the copies of 32 rows: the tile's rows 0..15 are
+// consecutive matrix rows, 16..31 start `skip` rows after the first. Offsets
+// are bytes from the tile's first row; an expert's matrix is below 2^31 bytes.
 template <int BITS, bool G16>
-__device__ __forceinline__ void issue_stage(const Packed& m, uint32_t dst,
-                                            int64_t base, int64_t base2, int c,
-                                            int lane) {
+struct Stream {
+  uint32_t code_off[BITS];  // the lane's 16-byte pieces of the codes
+  uint32_t row_off;         // entries from the first row to the lane's row
+  const uint8_t* codes;     // of the tile's first row, at the next chunk
+  const float* delta;       // of the lane's row
+  const uint8_t* zero;
+  int c;                    // the next chunk
+
+  __device__ __forceinline__ Stream(const Packed& m, int skip, int lane) {
 #pragma unroll
-  for (int i = 0; i < BITS; ++i) {
-    const int p = lane + 32 * i, r = p / BITS, pc = p % BITS;
-    const int64_t row = r < 16 ? base + r : base2 + (r - 16);
-    const int word = (c * BITS + pc) * 4;
-    if (word < m.ldc)
-      cp_async_16(dst + r * kPitch<BITS> + pc * 16,
-                  m.codes + row * m.ldc + word);
-  }
-  const int64_t row = lane < 16 ? base + lane : base2 + (lane - 16);
-  const uint32_t dd = dst + kStageCodes<BITS>;
-  if constexpr (G16) {
-    const float* d = m.delta + row * m.ldg + c * 8;
-    cp_async_16(dd + lane * 32, d);
-    cp_async_16(dd + lane * 32 + 16, d + 4);
-    cp_async_ca<8>(dd + kStageDelta + lane * 8, m.zero + row * m.ldg + c * 8);
-  } else {
-    const float* d = m.delta + row * m.ldg;
-    const uint8_t* z = m.zero + row * m.ldg;
-    if (m.group == 32) {
-      cp_async_16(dd + lane * 16, d + c * 4);
-    } else if (m.group == 64) {
-      cp_async_ca<8>(dd + lane * 16, d + c * 2);
-    } else {
-      cp_async_ca<4>(dd + lane * 16, d + c);
+    for (int i = 0; i < BITS; ++i) {
+      const int p = lane + 32 * i, r = p / BITS;
+      code_off[i] =
+          (uint32_t)(r < 16 ? r : skip + r - 16) * (uint32_t)m.ldc * 4u +
+          (uint32_t)(p % BITS) * 16u;
     }
-    // the aligned word that holds the stage's zero points
-    const int g0 = c * (kChunk / m.group);
-    cp_async_ca<4>(dd + kRows * 16 + lane * 4, z + (g0 & ~3));
+    row_off = (uint32_t)(lane < 16 ? lane : skip + lane - 16) *
+              (uint32_t)m.ldg;
   }
-}
+  // To chunk c0 of the tile whose first matrix row is `row`.
+  __device__ __forceinline__ void seek(const Packed& m, int64_t row, int c0) {
+    codes = reinterpret_cast<const uint8_t*>(m.codes + row * m.ldc) +
+            (int64_t)c0 * (16 * BITS);
+    delta = m.delta + row * m.ldg + row_off;
+    zero = m.zero + row * m.ldg + row_off;
+    c = c0;
+  }
+  // Issues the copies of the next chunk and moves on.
+  __device__ __forceinline__ void copy(const Packed& m, uint32_t dst,
+                                       int lane) {
+    const int left = m.ldc - c * (4 * BITS);  // words of the row from here
+    if (left >= 4 * BITS) {
+#pragma unroll
+      for (int i = 0; i < BITS; ++i) {
+        const int p = lane + 32 * i;
+        cp_async_16(dst + p / BITS * kPitch<BITS> + p % BITS * 16,
+                    codes + code_off[i]);
+      }
+    } else {  // the row ends inside the chunk
+#pragma unroll
+      for (int i = 0; i < BITS; ++i) {
+        const int p = lane + 32 * i;
+        if (p % BITS * 4 < left)
+          cp_async_16(dst + p / BITS * kPitch<BITS> + p % BITS * 16,
+                      codes + code_off[i]);
+      }
+    }
+    // the pitch of delta and zero is a multiple of 16 entries: a chunk's are
+    // always there
+    const uint32_t dd = dst + kStageCodes<BITS>;
+    if constexpr (G16) {
+      cp_async_16(dd + lane * 32, delta + c * 8);
+      cp_async_16(dd + lane * 32 + 16, delta + c * 8 + 4);
+      cp_async_ca<8>(dd + kStageDelta + lane * 8, zero + c * 8);
+    } else {
+      int g0 = c;
+      if (m.group == 32) {
+        g0 = c * 4;
+        cp_async_16(dd + lane * 16, delta + g0);
+      } else if (m.group == 64) {
+        g0 = c * 2;
+        cp_async_ca<8>(dd + lane * 16, delta + g0);
+      } else {
+        cp_async_ca<4>(dd + lane * 16, delta + g0);
+      }
+      // the aligned word that holds the chunk's zero points
+      cp_async_ca<4>(dd + kRows * 16 + lane * 4, zero + (g0 & ~3));
+    }
+    codes += 16 * BITS;
+    ++c;
+  }
+};
 
 // ----------------------------------------------------------- unpacking ---
 
@@ -257,44 +298,18 @@ __device__ __forceinline__ float ldsf(uint32_t a) {
   return __uint_as_float(lds32(a));
 }
 
-// How a code pair enters the MMA. NORM: as 1024 + q (the code in the mantissa
-// of 1024), from which the caller takes 1024 + z. Otherwise as the subnormal
-// q << kAt: the tensor core lines its products up by exponent and does not
-// normalise subnormal operands, so a code at bit 0 would lose 10 - b bits of
-// the sum (measured: 2-bit codes at bit 0 gave 5e-5 relative error, at bit 6
-// 2e-6). The top is 10 - b; up to 3 bits less are taken where that saves a
-// shift.
-template <int BITS>
-constexpr int kAt = BITS <= 3 ? 6 : BITS == 4 ? 4 : BITS == 5 ? 5
-                                : BITS == 6 ? 3 : 0;
 template <int BITS>
 constexpr uint32_t kMask = ((1u << BITS) - 1u) * 0x10001u;
 
-// The code pair whose codes start at bit FROM of both halves of m.
-template <int BITS, bool NORM, int FROM>
+// The code pair I of a lane's block, from `m` whose halves hold the fields'
+// codes from bit FROM on. NORM: as 1024 + q, from which the caller takes
+// 1024 + z. Otherwise the subnormal at Positions' bit.
+template <int BITS, bool G16, bool NORM, int I, int FROM>
 __device__ __forceinline__ uint32_t pair_at(uint32_t m) {
   if constexpr (NORM) return ((m >> FROM) & kMask<BITS>) | 0x64006400u;
-  constexpr int to = kAt<BITS>;
-  if constexpr (FROM < to) return (m << (to - FROM)) & (kMask<BITS> << to);
-  return (m >> (FROM < to ? 0 : FROM - to)) & (kMask<BITS> << to);
-}
-
-// Four registers of code pairs from two fields of four
-// codes: (u0, v0), (u1, v1), (u2, v2), (u3, v3).
-template <int BITS, bool NORM>
-__device__ __forceinline__ void pairs4(uint32_t u, uint32_t v,
-                                       uint32_t (&p)[4]) {
-  const uint32_t m = __byte_perm(u, v, 0x5410);
-  p[0] = pair_at<BITS, NORM, 0>(m);
-  p[1] = pair_at<BITS, NORM, BITS>(m);
-  if constexpr (BITS <= 4) {
-    p[2] = pair_at<BITS, NORM, 2 * BITS>(m);
-    p[3] = pair_at<BITS, NORM, 3 * BITS>(m);
-  } else {
-    const uint32_t n = __byte_perm(u >> (2 * BITS), v >> (2 * BITS), 0x5410);
-    p[2] = pair_at<BITS, NORM, 0>(n);
-    p[3] = pair_at<BITS, NORM, BITS>(n);
-  }
+  constexpr int to = Positions<BITS, G16>::at(I);
+  static_assert(to <= FROM, "codes move down");
+  return (m >> (FROM - to)) & (kMask<BITS> << to);
 }
 
 // Where a lane (t = lane % 4) finds its codes in a block of BITS words.
@@ -322,44 +337,60 @@ struct Field {
       sh2 = 0;
     }
   }
+  template <int I, int FROM>
+  static __device__ __forceinline__ uint32_t pair(uint32_t m) {
+    return pair_at<BITS, G16, NORM, I, FROM>(m);
+  }
   // p[0], p[1] feed the block's first MMA, p[2], p[3] its second.
   __device__ __forceinline__ void codes(uint32_t at, uint32_t (&p)[4]) const {
     if constexpr (G16) {
+      // pairs (0, 2), (1, 3) of each half's four codes
       uint32_t u = lds32(at + w0), v = lds32(at + w2);
-      if constexpr (BITS == 8) {
-      } else {
+      if constexpr (BITS != 8) {
         u = __funnelshift_r(u, lds32(at + w1), sh);
         v = __funnelshift_r(v, lds32(at + w3), sh2);
       }
       const uint32_t m = __byte_perm(u, u >> (2 * BITS), 0x5410);
       const uint32_t n = __byte_perm(v, v >> (2 * BITS), 0x5410);
-      p[0] = pair_at<BITS, NORM, 0>(m);
-      p[1] = pair_at<BITS, NORM, BITS>(m);
-      p[2] = pair_at<BITS, NORM, 0>(n);
-      p[3] = pair_at<BITS, NORM, BITS>(n);
-    } else if constexpr (BITS == 4) {
-      const uint32_t m = lds32(at + w0);
-      p[0] = pair_at<4, NORM, 0>(m);
-      p[1] = pair_at<4, NORM, 4>(m);
-      p[2] = pair_at<4, NORM, 8>(m);
-      p[3] = pair_at<4, NORM, 12>(m);
-    } else if constexpr (BITS == 8) {
-      pairs4<8, NORM>(lds32(at + w0), lds32(at + w1), p);
-    } else if constexpr (BITS == 2) {
-      const uint32_t u = lds32(at + w0) >> sh;
-      pairs4<2, NORM>(u, u >> 8, p);
-    } else if constexpr (BITS == 3) {
-      const uint32_t u = __funnelshift_r(lds32(at + w0), lds32(at + w1), sh);
-      pairs4<3, NORM>(u, u >> 12, p);
+      p[0] = pair<0, 0>(m);
+      p[1] = pair<1, BITS>(m);
+      p[2] = pair<2, 0>(n);
+      p[3] = pair<3, BITS>(n);
     } else {
-      const uint32_t a = lds32(at + w0), b = lds32(at + w1);
-      const uint32_t lo = __funnelshift_r(a, b, sh);
-      uint32_t hi;
-      if constexpr (BITS == 7)
-        hi = __funnelshift_r(b, lds32(at + w2), sh);
-      else
-        hi = b >> sh;
-      pairs4<BITS, NORM>(lo, __funnelshift_r(lo, hi, 4 * BITS), p);
+      // u: codes 0..3, v: codes 4..7 from bit 0 on; pairs (i, i + 4)
+      uint32_t u, v;
+      if constexpr (BITS == 2) {
+        u = lds32(at + w0) >> sh;
+        v = u >> 8;
+      } else if constexpr (BITS == 3) {
+        u = __funnelshift_r(lds32(at + w0), lds32(at + w1), sh);
+        v = u >> 12;
+      } else if constexpr (BITS == 4) {
+        u = lds32(at + w0);
+        v = u >> 16;
+      } else if constexpr (BITS == 8) {
+        u = lds32(at + w0);
+        v = lds32(at + w1);
+      } else {
+        const uint32_t a = lds32(at + w0), b = lds32(at + w1);
+        u = __funnelshift_r(a, b, sh);
+        const uint32_t hi = BITS == 7 ? __funnelshift_r(b, lds32(at + w2), sh)
+                                      : b >> sh;
+        v = __funnelshift_r(u, hi, 4 * BITS);
+      }
+      const uint32_t m = BITS == 4 ? u : __byte_perm(u, v, 0x5410);
+      p[0] = pair<0, 0>(m);
+      p[1] = pair<1, BITS>(m);
+      if constexpr (BITS <= 4) {
+        p[2] = pair<2, 2 * BITS>(m);
+        p[3] = pair<3, 3 * BITS>(m);
+      } else {
+        const uint32_t n =
+            BITS == 8 ? __byte_perm(u, v, 0x7632)
+                      : __byte_perm(u >> (2 * BITS), v >> (2 * BITS), 0x5410);
+        p[2] = pair<2, 0>(n);
+        p[3] = pair<3, BITS>(n);
+      }
     }
   }
 };
@@ -373,30 +404,52 @@ __device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0,
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-constexpr uint32_t kOnes = 0x3C003C00u;  // (1, 1)
-// what a code's unit is in the accumulators, and its inverse
-template <int BITS, int TERMS>
+// What the kernels do with the activations' precision.
+//   kOne: one fp16 term, for a bf16 Y.
+//   kTwo: two fp16 terms (22 bits), for an fp16 Y.
+//   kExact: two terms, and z taken from the codes before the MMA, with the
+//     codes as normal numbers, for an fp32 Y: subnormal operands are not
+//     normalised before the tensor core lines its products up, which costs up
+//     to 10 - b bits of the sum (measured: 5e-5 relative error for 2-bit codes
+//     at bit 0), and sum q x and z sum x cancel by a few bits more.
+enum Mode { kOne = 1, kTwo = 2, kExact = 3 };
+
+template <int MODE>
+constexpr int kTerms = MODE == kOne ? 1 : 2;
+
+// what a code's unit is in the accumulators
+template <int BITS, bool G16, int MODE>
 constexpr float kUnit =
-    TERMS == 2 ? 1.f : (float)(1 << kAt<BITS>) / 16777216.f;
-template <int BITS, int TERMS>
-constexpr float kPerUnit = 1.f / kUnit<BITS, TERMS>;
+    MODE == kExact
+        ? 1.f
+        : (float)(1 << Positions<BITS, G16>::kMost) / 16777216.f;
 
 __device__ __forceinline__ void subtract(uint32_t& p, __half2 z) {
   const __half2 d = __hsub2(*reinterpret_cast<const __half2*>(&p), z);
   p = *reinterpret_cast<const uint32_t*>(&d);
 }
 
-// One stage's products into acc[row tile][column tile]. x(n, b, v) gives the
-// lane's 8 activations of block b for column tile n, a uint4 per term: x, y
-// for the block's first MMA, z, w for its second.
-template <int BITS, bool G16, int TERMS, int NT, int NTMAX, typename XF>
+// 2^-(kMost - at(i)) in both halves: the weights of the sum of x.
+template <int BITS, bool G16>
+__host__ __device__ constexpr uint32_t ones(int i) {
+  return (uint32_t)(15 - (Positions<BITS, G16>::kMost -
+                          Positions<BITS, G16>::at(i)))
+         << 10 | (uint32_t)(15 - (Positions<BITS, G16>::kMost -
+                                  Positions<BITS, G16>::at(i)))
+         << 26;
+}
+
+// One stage's products into acc[row tile][column tile]. xp[n] (and xp[n] +
+// term for the second term) points at the lane's activations of the stage: 16
+// bytes per 32-channel block, 64 bytes apart, .x and .y for the block's first
+// MMA, .z and .w for its second.
+template <int BITS, bool G16, int MODE, int NT, int NTMAX>
 __device__ __forceinline__ void stage_products(
-    uint32_t st, const Field<BITS, G16, TERMS == 2>& f, int group, int c, int nblocks,
-    XF&& x, float (&acc)[2][NTMAX][4], int lane) {
-  // With two terms the sums are to be good to fp32: z is taken from the codes
-  // (exact in fp16), so that sum q x and z sum x never cancel. With one term
-  // it is cheaper to take it from the sums.
-  constexpr bool kCentre = TERMS == 2;
+    uint32_t st, const Field<BITS, G16, MODE == kExact>& f, int group, int c,
+    int nblocks, const uint4* const (&xp)[NTMAX], int64_t term,
+    uint4 (&xv)[NTMAX][kTerms<MODE>], float (&acc)[2][NTMAX][4], int lane) {
+  constexpr int TERMS = kTerms<MODE>;
+  constexpr bool kCentre = MODE == kExact;
   const int g = lane >> 2;
   const uint32_t dd = st + kStageCodes<BITS>;
   float cc[2][NT][4], s[NT][4];
@@ -423,7 +476,13 @@ __device__ __forceinline__ void stage_products(
 #pragma unroll
       for (int i = 0; i < 4; ++i) cc[0][n][i] = cc[1][n][i] = s[n][i] = 0.f;
   };
-  // acc += D (c - z s) for group j of the stage; z0, z1 hold -z in units
+  // -z in units: 2^23 + z by one OR, and one exact fused multiply-add
+  auto minus_z = [&](int r, int j) -> float {
+    constexpr float u = kUnit<BITS, G16, MODE>;
+    return fmaf(__uint_as_float(0x4B000000u | zero_at(r, j)), -u,
+                8388608.f * u);
+  };
+  // acc += D (c - z s) for group j of the stage
   auto flush = [&](int j) {
 #pragma unroll
     for (int rt = 0; rt < 2; ++rt) {
@@ -433,8 +492,8 @@ __device__ __forceinline__ void stage_products(
       const float d1 = ldsf(dd + (r + 8) * pitch + j * 4);
       float z0 = 0.f, z1 = 0.f;
       if constexpr (!kCentre) {
-        z0 = zero_at(r, j) * -kUnit<BITS, TERMS>;
-        z1 = zero_at(r + 8, j) * -kUnit<BITS, TERMS>;
+        z0 = minus_z(r, j);
+        z1 = minus_z(r + 8, j);
       }
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
@@ -456,14 +515,25 @@ __device__ __forceinline__ void stage_products(
     for (int rt = 0; rt < 2; ++rt)
       mma_f16(cc[rt][n], p[rt][0][2 * h], p[rt][1][2 * h],
               p[rt][0][2 * h + 1], p[rt][1][2 * h + 1], b0, b1);
-    if constexpr (!kCentre)
-      mma_f16(s[n], kOnes, kOnes, kOnes, kOnes, b0, b1);
+    if constexpr (!kCentre) {
+      const uint32_t o0 = ones<BITS, G16>(2 * h);
+      const uint32_t o1 = ones<BITS, G16>(2 * h + 1);
+      mma_f16(s[n], o0, o0, o1, o1, b0, b1);
+    }
   };
   clear();
   const int bpg = G16 ? 1 : group >> 5;  // blocks per group
 #pragma unroll
   for (int b = 0; b < 4; ++b) {
     if (b < nblocks) {
+      // the next block's activations
+      uint4 xn[NT][TERMS];
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int k = 0; k < TERMS; ++k)
+          if (b < 3 && b + 1 < nblocks)
+            xn[n][k] = xp[n][k * term + (b + 1) * 4];
       uint32_t p[2][2][4];  // [row tile][row g, row g + 8][pair]
       if (!G16 && b % bpg == 0) centre(b / bpg);
 #pragma unroll
@@ -474,13 +544,11 @@ __device__ __forceinline__ void stage_products(
         f.codes(at + 8 * kPitch<BITS>, p[rt][1]);
         if constexpr (kCentre && !G16) {
 #pragma unroll
-          for (int i = 0; i < 8; ++i) subtract(p[rt][i >> 2][i & 3], zc[rt][i >> 2]);
+          for (int i = 0; i < 8; ++i)
+            subtract(p[rt][i >> 2][i & 3], zc[rt][i >> 2]);
         }
       }
       if constexpr (G16) {
-        uint4 xv[NT][TERMS];
-#pragma unroll
-        for (int n = 0; n < NT; ++n) x(n, b, xv[n]);
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           if constexpr (kCentre) {
@@ -491,46 +559,34 @@ __device__ __forceinline__ void stage_products(
                        zc[i >> 2][(i >> 1) & 1]);
           }
 #pragma unroll
-          for (int n = 0; n < NT; ++n) {
+          for (int n = 0; n < NT; ++n)
 #pragma unroll
             for (int k = 0; k < TERMS; ++k)
               products(p, h, n, h ? xv[n][k].z : xv[n][k].x,
                        h ? xv[n][k].w : xv[n][k].y);
-          }
           flush(2 * b + h);
           clear();
         }
       } else {
 #pragma unroll
-        for (int n = 0; n < NT; ++n) {
-          uint4 xv[TERMS];
-          x(n, b, xv);
+        for (int h = 0; h < 2; ++h)
 #pragma unroll
-          for (int k = 0; k < TERMS; ++k) {
-            products(p, 0, n, xv[k].x, xv[k].y);
-            products(p, 1, n, xv[k].z, xv[k].w);
-          }
-        }
-      }
-      if constexpr (!G16) {
+          for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int k = 0; k < TERMS; ++k)
+              products(p, h, n, h ? xv[n][k].z : xv[n][k].x,
+                       h ? xv[n][k].w : xv[n][k].y);
         if ((b + 1) % bpg == 0) {
           flush(b / bpg);
           if (b < 3) clear();
         }
       }
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int k = 0; k < TERMS; ++k) xv[n][k] = xn[n][k];
     }
   }
-}
-
-// 2^k with the row's largest value (its bits) brought into [2^13, 2^14); the
-// exponent is kept in the normal range.
-__device__ __forceinline__ float row_scale(uint32_t max_bits) {
-  const int e = (int)(max_bits >> 23) - 127;
-  return __uint_as_float((uint32_t)(127 + min(13 - e, 126)) << 23);
-}
-__device__ __forceinline__ float row_unscale(uint32_t max_bits) {
-  const int e = (int)(max_bits >> 23) - 127;
-  return __uint_as_float((uint32_t)(127 - min(13 - e, 126)) << 23);
 }
 
 __device__ __forceinline__ float gated(float g, int act) {
@@ -557,150 +613,209 @@ __device__ __forceinline__ float ld_cluster_f32(uint32_t a, uint32_t rank) {
   return v;
 }
 
-__device__ __forceinline__ uint32_t half2_bits(float a, float b) {
-  const __half2 h = __floats2half2_rn(a, b);
-  return *reinterpret_cast<const uint32_t*>(&h);
+// 2^-k of the scale the rows carry (rows_kernel in moe.cu).
+__device__ __forceinline__ float row_unscale(uint32_t max_bits, int most) {
+  return __uint_as_float((uint32_t)(127 - row_exponent(max_bits, most)) << 23);
 }
+
+// One warp's walk through its stages: x rows, products.
+template <int BITS, bool G16, int MODE, int NTMAX>
+struct Tile {
+  static constexpr int TERMS = kTerms<MODE>;
+  static constexpr int S = kStages<BITS>, kSt = kStage<BITS, G16>;
+  const Field<BITS, G16, MODE == kExact> f;
+  uint32_t ring;
+  int lane, nt;
+  const uint4* xp[NTMAX];  // the lane's activations at the next stage
+  int64_t term;
+  float acc[2][NTMAX][4];
+
+  __device__ __forceinline__ Tile(uint32_t ring_, int lane_, int64_t term_)
+      : f(lane_ & 3), ring(ring_), lane(lane_), term(term_) {}
+
+  // Starts a tile with `cols` columns; row(col) gives a column's activations
+  // (columns past the last repeat column 0: their results are dropped).
+  template <typename RF>
+  __device__ __forceinline__ void start(int cols, int c, RF&& row) {
+    nt = (cols + 7) / 8;
+#pragma unroll
+    for (int n = 0; n < NTMAX; ++n) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) acc[0][n][i] = acc[1][n][i] = 0.f;
+      const int col = n * 8 + (lane >> 2);
+      xp[n] = row(col < cols ? col : 0) + c * 16 + (lane & 3);
+    }
+  }
+  template <int NT>
+  __device__ __forceinline__ void fetch(uint4 (&xv)[NTMAX][TERMS]) {
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int k = 0; k < TERMS; ++k) xv[n][k] = xp[n][k * term];
+  }
+  // One stage; next() issues the copies that refill the ring.
+  template <int NT, typename NF>
+  __device__ __forceinline__ void step_nt(const Packed& m, int c, int slot,
+                                          NF&& next) {
+    uint4 xv[NTMAX][TERMS];
+    fetch<NT>(xv);
+    cp_async_wait<S - 2>();
+    __syncwarp();  // the stage is there, and every lane has left the last one
+    next();
+    stage_products<BITS, G16, MODE, NT, NTMAX>(
+        ring + slot * kSt, f, m.group, c, min(4, m.blocks - 4 * c), xp, term,
+        xv, acc, lane);
+#pragma unroll
+    for (int n = 0; n < NT; ++n) xp[n] += 16;
+  }
+  template <typename NF>
+  __device__ __forceinline__ void step(const Packed& m, int c, int slot,
+                                       NF&& next) {
+    if (NTMAX == 1 || nt == 1)
+      step_nt<1>(m, c, slot, next);
+    else
+      step_nt<NTMAX>(m, c, slot, next);
+  }
+};
 
 // ------------------------------------------------------------------ up ---
 
-// Units of 16 intermediate channels (16 gate rows and the 16 rows of the
-// other factor) of one entry, taken round robin by a persistent grid; the
-// warps split K.
-template <int BITS, bool G16, int TERMS, int NTMAX>
+// A warp's tile is 16 intermediate channels: their 16 gate rows and the 16
+// rows of the other factor, which end in the same lanes and registers. The
+// CTA's 8 warps are `rs` neighbouring tiles of one entry times 8 / rs parts
+// of K; units (entry, rs tiles) are taken round robin by a persistent grid.
+// Neighbouring tiles share their activations through L1; parts of K are added
+// through shared memory.
+template <int BITS, bool G16, int MODE, int NTMAX>
 __global__ void __launch_bounds__(kThreads, 2)
     up_kernel(const UpArgs a) {
-  constexpr int S = kStages<BITS>, kSt = kStage<BITS, G16>;
-  constexpr int kRedTiles = NTMAX < 2 ? NTMAX : 2;  // column tiles reduced at once
+  using TileT = Tile<BITS, G16, MODE, NTMAX>;
+  constexpr int S = TileT::S, kSt = TileT::kSt;
   extern __shared__ __align__(16) uint8_t sm[];
   Lists l(sm, a.T * a.top_k, a.E);
-  float* red =
+  float* red =  // [warp][row tile][column tile][128]
       reinterpret_cast<float*>(sm + Lists::bytes(a.T * a.top_k, a.E));
-  // [warp][row tile][column tile][128]
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const uint32_t ring =
-      smem_u32(red) + kWarps * 2 * kRedTiles * 128 * 4 + warp * S * kSt;
+      smem_u32(red) + kWarps * 2 * NTMAX * 128 * 4 + warp * S * kSt;
 
   // ids and the packed weights were complete before the kernel that runs
   // before this one started: lists and the first stages need not wait for it
   build_lists(l, a.ids, nullptr, a.T, a.top_k, a.E, a.err);
-  const int tiles = a.I / 16, units = l.entries * tiles;
+  const int rs = a.rs, ks = kWarps / rs;
+  const int wr = warp % rs, wk = warp / rs;
+  const int tiles = a.I / 16, rows = (tiles + rs - 1) / rs;
+  const int units = l.entries * rows;
   const int chunks = (a.K + kChunk - 1) / kChunk;
-  const int c0 = warp * chunks / kWarps, c1 = (warp + 1) * chunks / kWarps;
+  const int c0 = wk * chunks / ks, c1 = (wk + 1) * chunks / ks;
   Packed m;
   m.codes = a.codes;
   m.delta = a.delta;
   m.zero = a.zero;
-  m.ldc = codes_ld(a.K, BITS);
-  m.ldg = groups_ld(a.K, a.group);
+  m.ldc = (int)codes_ld(a.K, BITS);
+  m.ldg = (int)groups_ld(a.K, a.group);
   m.blocks = a.K / 32;
   m.group = a.group;
-  const Field<BITS, G16, TERMS == 2> f(lane & 3);
+  Stream<BITS, G16> w(m, a.I, lane);
 
   // the warp's stages: its chunks of the CTA's units, one after the other
-  int iu = blockIdx.x, ic = c0, ist = 0;
+  int iu = blockIdx.x, ist = 0;
+  auto seek = [&]() {
+    // the warp's tile of unit iu, skipping units in which it has none
+    for (; iu < units && c0 < c1; iu += gridDim.x) {
+      const int en = iu / rows, tile = (iu - en * rows) * rs + wr;
+      if (tile < tiles) {
+        w.seek(m, (int64_t)l.expert[en] * 2 * a.I + tile * 16, c0);
+        return;
+      }
+    }
+    iu = units;
+  };
   auto issue = [&]() {
-    if (iu < units && c0 < c1) {
-      const int en = iu / tiles, tile = iu - en * tiles;
-      const int64_t base =
-          (int64_t)l.expert[en] * 2 * a.I + tile * 16;
-      issue_stage<BITS, G16>(m, ring + ist * kSt, base, base + a.I, ic, lane);
-      if (++ic == c1) {
-        ic = c0;
+    if (iu < units) {
+      w.copy(m, ring + ist * kSt, lane);
+      if (w.c == c1) {
         iu += gridDim.x;
+        seek();
       }
     }
     cp_async_commit();
     ist = ist + 1 == S ? 0 : ist + 1;
   };
+  seek();
 #pragma unroll
   for (int i = 0; i < S - 1; ++i) issue();
   griddep_enter();
 
+  TileT tl(ring, lane, (int64_t)a.T * a.K / 8);
   int cst = 0;
-  const int t = lane & 3;
   for (int u = blockIdx.x; u < units; u += gridDim.x) {
-    const int en = u / tiles, tile = u - en * tiles;
+    const int en = u / rows, tile = (u - en * rows) * rs + wr;
     const int cols = l.cols[en], col0 = l.first[en];
-    const int nt = (cols + 7) / 8;
-    float acc[2][NTMAX][4];
-#pragma unroll
-    for (int n = 0; n < NTMAX; ++n)
-#pragma unroll
-      for (int i = 0; i < 4; ++i) acc[0][n][i] = acc[1][n][i] = 0.f;
-    // this lane's column of each tile; columns past the last repeat column
-    // 0, whose results are dropped
-    const uint4* xr[NTMAX];
-#pragma unroll
-    for (int n = 0; n < NTMAX; ++n) {
-      const int col = n * 8 + (lane >> 2);
-      const int tok = l.slot[col0 + (col < cols ? col : 0)] / a.top_k;
-      xr[n] = reinterpret_cast<const uint4*>(a.xhat + (int64_t)tok * a.K) + t;
-    }
-    const int64_t term = (int64_t)a.T * a.K / 8;  // in uint4
-    for (int c = c0; c < c1; ++c) {
-      cp_async_wait<S - 2>();
-      __syncwarp();  // and every lane is done with the stage before
-      issue();
-      const uint32_t st = ring + cst * kSt;
-      const int nb = min(4, m.blocks - 4 * c);
-      auto x = [&](int n, int b, uint4 (&v)[TERMS]) {
-#pragma unroll
-        for (int k = 0; k < TERMS; ++k)
-          v[k] = xr[n][k * term + (c * 4 + b) * 4];
-      };
-      if (NTMAX == 1 || nt == 1)
-        stage_products<BITS, G16, TERMS, 1, NTMAX>(st, f, a.group, c, nb, x,
-                                                   acc, lane);
-      else if (NTMAX == 2 || nt == 2)
-        stage_products<BITS, G16, TERMS, (NTMAX < 2 ? NTMAX : 2), NTMAX>(
-            st, f, a.group, c, nb, x, acc, lane);
-      else
-        stage_products<BITS, G16, TERMS, NTMAX, NTMAX>(st, f, a.group, c, nb,
-                                                       x, acc, lane);
-      cst = cst + 1 == S ? 0 : cst + 1;
-    }
-    // add the warps' sums, kRedTiles column tiles at a time
-#pragma unroll
-    for (int n0 = 0; n0 < NTMAX; n0 += kRedTiles) {
-      if (n0 >= nt) break;
-      __syncthreads();  // the last round's sums have been read
-#pragma unroll
-      for (int rt = 0; rt < 2; ++rt)
-#pragma unroll
-        for (int n = 0; n < kRedTiles; ++n)
-          *reinterpret_cast<float4*>(
-              red + ((warp * 2 + rt) * kRedTiles + n) * 128 + lane * 4) =
-              make_float4(acc[rt][n0 + n][0], acc[rt][n0 + n][1],
-                          acc[rt][n0 + n][2], acc[rt][n0 + n][3]);
-      __syncthreads();
-      const int n = tid >> 7, i = tid & 127;
-      // element i of a tile: lane i / 4, register i % 4
-      const int row = (i >> 4) + 8 * ((i >> 1) & 1);
-      const int col = (n0 + n) * 8 + 2 * ((i >> 2) & 3) + (i & 1);
-      float hv = 0.f;
-      int slot = 0;
-      const bool live = n < kRedTiles && col < cols;
-      if (live) {
-        float gs = 0.f, us = 0.f;
-#pragma unroll
-        for (int w = 0; w < kWarps; ++w) {
-          gs += red[((w * 2 + 0) * kRedTiles + n) * 128 + i];
-          us += red[((w * 2 + 1) * kRedTiles + n) * 128 + i];
-        }
-        slot = l.slot[col0 + col];
-        const float un = row_unscale(a.xmax[slot / a.top_k]);
-        const int ch = tile * 16 + row;
-        hv = gated(gs * kPerUnit<BITS, TERMS> * un, a.act) * (us * kPerUnit<BITS, TERMS> * un) *
-             a.inv_s_mid[(int64_t)l.expert[en] * a.I + ch];
-        a.h[(int64_t)slot * a.I + ch] = hv;
+    const bool live = tile < tiles;
+    tl.start(cols, c0, [&](int col) {
+      return a.xhat + (int64_t)(l.slot[col0 + col] / a.top_k) * (a.K / 8);
+    });
+    if (live) {
+      for (int c = c0; c < c1; ++c) {
+        tl.step(m, c, cst, issue);
+        cst = cst + 1 == S ? 0 : cst + 1;
       }
-      // the slot's largest |h|: rows of one column sit in lanes that differ
-      // in bits 1 and 4 (all lanes of a warp hold the same n)
-      uint32_t mx = __float_as_uint(hv) & 0x7FFFFFFFu;
-      mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-      mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
-      if (live && (lane & 18) == 0) atomicMax(a.hmax + slot, mx);
+    }
+    if (ks > 1) {
+      // parts of K to the warp of part 0
+      __syncthreads();  // the last sums have been read
+      if (wk > 0) {
+#pragma unroll
+        for (int rt = 0; rt < 2; ++rt)
+#pragma unroll
+          for (int n = 0; n < NTMAX; ++n)
+            *reinterpret_cast<float4*>(
+                red + ((warp * 2 + rt) * NTMAX + n) * 128 + lane * 4) =
+                make_float4(tl.acc[rt][n][0], tl.acc[rt][n][1],
+                            tl.acc[rt][n][2], tl.acc[rt][n][3]);
+      }
+      __syncthreads();
+      if (wk == 0) {
+        for (int k = 1; k < ks; ++k) {
+          const int from = k * rs + wr;
+#pragma unroll
+          for (int rt = 0; rt < 2; ++rt)
+#pragma unroll
+            for (int n = 0; n < NTMAX; ++n) {
+              const float4 v = *reinterpret_cast<const float4*>(
+                  red + ((from * 2 + rt) * NTMAX + n) * 128 + lane * 4);
+              tl.acc[rt][n][0] += v.x;
+              tl.acc[rt][n][1] += v.y;
+              tl.acc[rt][n][2] += v.z;
+              tl.acc[rt][n][3] += v.w;
+            }
+        }
+      }
+    }
+    if (wk == 0 && live) {
+      constexpr float per_unit = 1.f / kUnit<BITS, G16, MODE>;
+      constexpr int most = MODE == kExact ? 0 : Positions<BITS, G16>::kMost;
+      const int ch = tile * 16 + (lane >> 2);
+      const float* mid = a.inv_s_mid + (int64_t)l.expert[en] * a.I + ch;
+      const float mid0 = mid[0], mid1 = mid[8];
+#pragma unroll
+      for (int n = 0; n < NTMAX; ++n) {
+        if (n >= tl.nt) break;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const int col = n * 8 + 2 * (lane & 3) + i;
+          if (col < cols) {
+            const int slot = l.slot[col0 + col];
+            const float un = row_unscale(a.xmax[slot / a.top_k], most);
+            float* h = a.h + (int64_t)slot * a.I + ch;
+            h[0] = gated(tl.acc[0][n][i] * per_unit * un, a.act) *
+                   (tl.acc[1][n][i] * per_unit * un) * mid0;
+            h[8] = gated(tl.acc[0][n][2 + i] * per_unit * un, a.act) *
+                   (tl.acc[1][n][2 + i] * per_unit * un) * mid1;
+          }
+        }
+      }
     }
   }
   cp_async_wait_all();
@@ -708,14 +823,16 @@ __global__ void __launch_bounds__(kThreads, 2)
 
 // ---------------------------------------------------------------- down ---
 
-// 32 output channels per cluster; the (entry, 128-channel chunk) pairs of the
-// batch are one list, split evenly over the warps of the cluster's CTAs.
-// Every warp keeps the sums of all tokens for its share and adds an entry's
-// columns to them when it leaves the entry.
-template <int BITS, bool G16, int TERMS, int NTMAX>
+// A warp's tile is 32 output channels; a CTA's 8 warps are `rs` neighbouring
+// tiles times 8 / rs parts. The (entry, 128-channel chunk) pairs of the batch
+// are one list, split evenly over the parts of all CTAs of a cluster. Every
+// warp keeps the sums of all tokens for its share and adds an entry's columns
+// to them when it leaves the entry; parts are added at the end, in order.
+template <int BITS, bool G16, int MODE, int NTMAX>
 __global__ void __launch_bounds__(kThreads, 2)
     down_kernel(const DownArgs a) {
-  constexpr int S = kStages<BITS>, kSt = kStage<BITS, G16>;
+  using TileT = Tile<BITS, G16, MODE, NTMAX>;
+  constexpr int S = TileT::S, kSt = TileT::kSt;
   extern __shared__ __align__(16) uint8_t sm[];
   Lists l(sm, a.T * a.top_k, a.E);
   float* ysum =  // [warp][T][32]
@@ -729,31 +846,35 @@ __global__ void __launch_bounds__(kThreads, 2)
   // before this one writes
   build_lists(l, a.ids, a.weights, a.T, a.top_k, a.E, nullptr);
   for (int i = lane; i < region; i += 32) mine[i] = 0.f;
+  const int rs = a.rs, ks = kWarps / rs;
+  const int wr = warp % rs, wk = warp / rs;
+  const int tile = blockIdx.x * rs + wr;
   const int chunks = (a.I + kChunk - 1) / kChunk;
-  const int total = l.entries * chunks;
+  const int total = tile * kRows < a.K ? l.entries * chunks : 0;
   const int ranks = gridDim.y, rank = blockIdx.y;
-  const int parts = ranks * kWarps, part = rank * kWarps + warp;
+  const int parts = ranks * ks, part = rank * ks + wk;
   const int s0 = (int)((int64_t)total * part / parts);
   const int s1 = (int)((int64_t)total * (part + 1) / parts);
-  const int n0 = blockIdx.x * kRows;
   Packed m;
   m.codes = a.codes;
   m.delta = a.delta;
   m.zero = a.zero;
-  m.ldc = codes_ld(a.I, BITS);
-  m.ldg = groups_ld(a.I, a.group);
+  m.ldc = (int)codes_ld(a.I, BITS);
+  m.ldg = (int)groups_ld(a.I, a.group);
   m.blocks = a.I / 32;
   m.group = a.group;
-  const Field<BITS, G16, TERMS == 2> f(lane & 3);
-  int is = s0, ien = s0 / chunks, ic = s0 - ien * chunks, ist = 0;
+  Stream<BITS, G16> w(m, 16, lane);
+  int is = s0, ien = s0 / chunks, ist = 0;
+  auto seek = [&](int c) {
+    w.seek(m, (int64_t)l.expert[ien] * a.K + tile * kRows, c);
+  };
+  if (s0 < s1) seek(s0 - ien * chunks);
   auto issue = [&]() {
     if (is < s1) {
-      const int64_t base = (int64_t)l.expert[ien] * a.K + n0;
-      issue_stage<BITS, G16>(m, ring + ist * kSt, base, base + 16, ic, lane);
-      ++is;
-      if (++ic == chunks) {
-        ic = 0;
+      w.copy(m, ring + ist * kSt, lane);
+      if (++is < s1 && w.c == chunks) {
         ++ien;
+        seek(0);
       }
     }
     cp_async_commit();
@@ -764,90 +885,37 @@ __global__ void __launch_bounds__(kThreads, 2)
   griddep_enter();
 
   const int t = lane & 3, g = lane >> 2;
+  TileT tl(ring, lane, (int64_t)a.T * a.top_k * a.I / 8);
   int s = s0, en = s0 / chunks, c = s0 - en * chunks, cst = 0;
   while (s < s1) {
     const int cols = l.cols[en], col0 = l.first[en];
-    const int nt = (cols + 7) / 8;
-    float acc[2][NTMAX][4];
-#pragma unroll
-    for (int n = 0; n < NTMAX; ++n)
-#pragma unroll
-      for (int i = 0; i < 4; ++i) acc[0][n][i] = acc[1][n][i] = 0.f;
-    const float* hr[NTMAX];
-    float sc[NTMAX];
-#pragma unroll
-    for (int n = 0; n < NTMAX; ++n) {
-      const int col = n * 8 + g;
-      const int slot = l.slot[col0 + (col < cols ? col : 0)];
-      hr[n] = a.h + (int64_t)slot * a.I;
-      sc[n] = row_scale(a.hmax[slot]);
-    }
+    tl.start(cols, c, [&](int col) {
+      return a.hhat + (int64_t)l.slot[col0 + col] * (a.I / 8);
+    });
     const int stop = min(s1, s + chunks - c);
     for (; s < stop; ++s, ++c) {
-      cp_async_wait<S - 2>();
-      __syncwarp();  // and every lane is done with the stage before
-      issue();
-      const uint32_t st = ring + cst * kSt;
-      const int nb = min(4, m.blocks - 4 * c);
-      auto x = [&](int n, int b, uint4 (&v)[TERMS]) {
-        const int at = (c * 4 + b) * 32 + (G16 ? 4 : 8) * t;
-        const float4 p = *reinterpret_cast<const float4*>(hr[n] + at);
-        const float4 q =
-            *reinterpret_cast<const float4*>(hr[n] + at + (G16 ? 16 : 4));
-        // in the order of the code pairs
-        float e[8];
-        if constexpr (G16) {
-          e[0] = p.x; e[1] = p.z; e[2] = p.y; e[3] = p.w;
-          e[4] = q.x; e[5] = q.z; e[6] = q.y; e[7] = q.w;
-        } else {
-          e[0] = p.x; e[1] = q.x; e[2] = p.y; e[3] = q.y;
-          e[4] = p.z; e[5] = q.z; e[6] = p.w; e[7] = q.w;
-        }
-        uint32_t r[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          e[2 * i] *= sc[n];
-          e[2 * i + 1] *= sc[n];
-          r[i] = half2_bits(e[2 * i], e[2 * i + 1]);
-        }
-        v[0] = make_uint4(r[0], r[1], r[2], r[3]);
-        if constexpr (TERMS == 2) {
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            float h0, h1;
-            f16x2_to_f32(r[i], h0, h1);
-            r[i] = half2_bits(e[2 * i] - h0, e[2 * i + 1] - h1);
-          }
-          v[1] = make_uint4(r[0], r[1], r[2], r[3]);
-        }
-      };
-      if (NTMAX == 1 || nt == 1)
-        stage_products<BITS, G16, TERMS, 1, NTMAX>(st, f, a.group, c, nb, x,
-                                                   acc, lane);
-      else if (NTMAX == 2 || nt == 2)
-        stage_products<BITS, G16, TERMS, (NTMAX < 2 ? NTMAX : 2), NTMAX>(
-            st, f, a.group, c, nb, x, acc, lane);
-      else
-        stage_products<BITS, G16, TERMS, NTMAX, NTMAX>(st, f, a.group, c, nb,
-                                                       x, acc, lane);
+      tl.step(m, c, cst, issue);
       cst = cst + 1 == S ? 0 : cst + 1;
     }
     // leave the entry: its columns are different tokens
+    constexpr float per_unit = 1.f / kUnit<BITS, G16, MODE>;
+    constexpr int most = MODE == kExact ? 0 : Positions<BITS, G16>::kMost;
 #pragma unroll
     for (int n = 0; n < NTMAX; ++n) {
-      if (n >= nt) break;
+      if (n >= tl.nt) break;
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         const int col = n * 8 + 2 * t + i;
         if (col < cols) {
           const int slot = l.slot[col0 + col];
-          const float w =
-              l.weight[col0 + col] * row_unscale(a.hmax[slot]) * kPerUnit<BITS, TERMS>;
+          const float wt =
+              l.weight[col0 + col] * row_unscale(a.hmax[slot], most) *
+              per_unit;
           float* y = mine + slot / a.top_k * kRows + g;
-          y[0] = fmaf(w, acc[0][n][i], y[0]);
-          y[8] = fmaf(w, acc[0][n][2 + i], y[8]);
-          y[16] = fmaf(w, acc[1][n][i], y[16]);
-          y[24] = fmaf(w, acc[1][n][2 + i], y[24]);
+          y[0] = fmaf(wt, tl.acc[0][n][i], y[0]);
+          y[8] = fmaf(wt, tl.acc[0][n][2 + i], y[8]);
+          y[16] = fmaf(wt, tl.acc[1][n][i], y[16]);
+          y[24] = fmaf(wt, tl.acc[1][n][2 + i], y[24]);
         }
       }
     }
@@ -857,28 +925,32 @@ __global__ void __launch_bounds__(kThreads, 2)
   }
   cp_async_wait_all();
   __syncthreads();
-  // add the warps' sums, then the CTAs' through distributed shared memory,
-  // both in order
-  for (int i = tid; i < region; i += kThreads) {
+  // add the CTA's parts, then the cluster's through distributed shared
+  // memory, both in order
+  for (int i = tid; i < rs * region; i += kThreads) {
     float v = ysum[i];
-#pragma unroll
-    for (int w = 1; w < kWarps; ++w) v += ysum[w * region + i];
+    for (int k = 1; k < ks; ++k) v += ysum[k * rs * region + i];
     ysum[i] = v;
   }
-  if (ranks > 1) cluster_sync(); else __syncthreads();
+  if (ranks > 1)
+    cluster_sync();
+  else
+    __syncthreads();
   const uint32_t ys = smem_u32(ysum);
-  for (int i = rank * kThreads + tid; i < region; i += ranks * kThreads) {
+  for (int i = rank * kThreads + tid; i < rs * region; i += ranks * kThreads) {
     float v = 0.f;
     if (ranks > 1) {
       for (int r = 0; r < ranks; ++r) v += ld_cluster_f32(ys + i * 4, r);
     } else {
       v = ysum[i];
     }
-    const int64_t at = (int64_t)(i / kRows) * a.ldy + n0 + i % kRows;
-    if constexpr (TERMS == 1) {
-      static_cast<__nv_bfloat16*>(a.Y)[at] = __float2bfloat16_rn(v);
-    } else {
-      if (a.yt == TTQ_F16)
+    const int q = i / region, e = i - q * region;
+    const int row = (blockIdx.x * rs + q) * kRows + e % kRows;
+    if (row < a.K) {
+      const int64_t at = (int64_t)(e / kRows) * a.ldy + row;
+      if constexpr (MODE == kOne)
+        static_cast<__nv_bfloat16*>(a.Y)[at] = __float2bfloat16_rn(v);
+      else if constexpr (MODE == kTwo)
         static_cast<__half*>(a.Y)[at] = __float2half_rn(v);
       else
         static_cast<float*>(a.Y)[at] = v;
@@ -891,7 +963,7 @@ __global__ void __launch_bounds__(kThreads, 2)
 
 template <int BITS, bool G16>
 size_t up_smem(int ntmax, int n, int E) {
-  return Lists::bytes(n, E) + (size_t)kWarps * 2 * std::min(ntmax, 2) * 128 * 4 +
+  return Lists::bytes(n, E) + (size_t)kWarps * 2 * ntmax * 128 * 4 +
          (size_t)kWarps * kStages<BITS> * kStage<BITS, G16>;
 }
 template <int BITS, bool G16>
@@ -907,46 +979,84 @@ bool allow_smem(K kern, size_t bytes) {
                               (int)bytes) == cudaSuccess;
 }
 
-template <int BITS, bool G16, int TERMS, int NTMAX>
-ttq_status launch_pair(const UpArgs& u, const DownArgs& d, cudaStream_t st) {
+// The rows a CTA's warps share out. More neighbouring tiles read an
+// activation once for more weights; fewer leave finer units to balance. Time
+// goes with rounds x rs; the largest rs within 10% of the best is taken.
+inline int pick_rs(int64_t tiles, int64_t slots) {
+  int64_t best = INT64_MAX;
+  for (int rs = 1; rs <= kWarps; rs *= 2) {
+    const int64_t units = (tiles + rs - 1) / rs;
+    best = std::min(best, (units + slots - 1) / slots * rs);
+  }
+  for (int rs = kWarps; rs > 1; rs /= 2) {
+    const int64_t units = (tiles + rs - 1) / rs;
+    if ((units + slots - 1) / slots * rs * 10 <= best * 11) return rs;
+  }
+  return 1;
+}
+
+inline int ctas_per_sm(size_t smem) { return smem + 1024 <= 114 * 1024 ? 2 : 1; }
+
+template <int BITS, bool G16, int MODE, int NTMAX>
+ttq_status launch_up(UpArgs u, cudaStream_t st) {
   LaunchShape ls;
   ls.block = dim3(kThreads);
   ls.smem = up_smem<BITS, G16>(NTMAX, u.T * u.top_k, u.E);
-  const int64_t per_sm = ls.smem + 1024 <= 114 * 1024 ? 2 : 1;
-  const int64_t units =
+  const int64_t slots = ctas_per_sm(ls.smem) * sm_count();
+  const int64_t tiles =
       (int64_t)Lists::max_entries(u.T * u.top_k, u.E) * (u.I / 16);
-  ls.grid = dim3((unsigned)std::min<int64_t>(units, per_sm * sm_count()));
-  auto up = up_kernel<BITS, G16, TERMS, NTMAX>;
-  if (!allow_smem(up, ls.smem)) return TTQ_ERR_CUDA;
-  const ttq_status s = launch(ls, st, up, u);
-  if (s != TTQ_OK) return s;
-  LaunchShape ld;
-  ld.block = dim3(kThreads);
-  ld.smem = down_smem<BITS, G16>(d.T, d.T * d.top_k, d.E);
-  const int tiles = (int)(d.K / kRows);
-  const int slots = (ld.smem + 1024 <= 114 * 1024 ? 2 : 1) * sm_count();
-  const int ranks = std::max(1, std::min(8, slots / tiles));
-  ld.grid = dim3((unsigned)tiles, (unsigned)ranks);
-  ld.cluster_y = (unsigned)ranks;
-  auto down = down_kernel<BITS, G16, TERMS, NTMAX>;
-  if (!allow_smem(down, ld.smem)) return TTQ_ERR_CUDA;
-  return launch(ld, st, down, d);
+  u.rs = pick_rs(tiles, slots);
+  ls.grid = dim3((unsigned)std::min<int64_t>(tiles, slots));
+  auto kern = up_kernel<BITS, G16, MODE, NTMAX>;
+  if (!allow_smem(kern, ls.smem)) return TTQ_ERR_CUDA;
+  return launch(ls, st, kern, u);
 }
 
-// TERMS: one fp16 term of the activations carries a bf16 output, two an fp16
-// or fp32 one. NTMAX: up to 8 tokens fill one column tile; more may put up to
-// 32 on one expert, which wants four.
-template <int BITS>
-ttq_status launch_bits(const UpArgs& u, const DownArgs& d, cudaStream_t st) {
+template <int BITS, bool G16, int MODE, int NTMAX>
+ttq_status launch_down(DownArgs d, cudaStream_t st) {
+  LaunchShape ls;
+  ls.block = dim3(kThreads);
+  ls.smem = down_smem<BITS, G16>(d.T, d.T * d.top_k, d.E);
+  const int slots = ctas_per_sm(ls.smem) * sm_count();
+  const int tiles = d.K / kRows;
+  // as many neighbouring tiles as still leave a cluster of up to 8 per SM slot
+  d.rs = kWarps;
+  while (d.rs > 1 && (tiles + d.rs - 1) / d.rs * 8 < slots) d.rs /= 2;
+  const int grid = (tiles + d.rs - 1) / d.rs;
+  const int ranks = std::max(1, std::min(8, slots / grid));
+  ls.grid = dim3((unsigned)grid, (unsigned)ranks);
+  ls.cluster_y = (unsigned)ranks;
+  auto kern = down_kernel<BITS, G16, MODE, NTMAX>;
+  if (!allow_smem(kern, ls.smem)) return TTQ_ERR_CUDA;
+  return launch(ls, st, kern, d);
+}
+
+// NTMAX: up to 8 tokens fill one column tile; more may put up to 16 on one
+// entry. (Four tiles did not fit the registers of two CTAs per SM: an expert
+// with more than 16 tokens becomes two entries, the second read from L2.)
+template <int BITS, bool G16, int MODE>
+ttq_status launch_mode(const UpArgs& u, cudaStream_t st) {
+  return u.T <= 8 ? launch_up<BITS, G16, MODE, 1>(u, st)
+                  : launch_up<BITS, G16, MODE, 2>(u, st);
+}
+template <int BITS, bool G16, int MODE>
+ttq_status launch_mode(const DownArgs& d, cudaStream_t st) {
+  return d.T <= 8 ? launch_down<BITS, G16, MODE, 1>(d, st)
+                  : launch_down<BITS, G16, MODE, 2>(d, st);
+}
+
+template <int BITS, typename Args>
+ttq_status launch_bits(const Args& a, cudaStream_t st) {
   auto go = [&](auto g16) -> ttq_status {
     constexpr bool G = decltype(g16)::value;
-    if (d.yt == TTQ_BF16)
-      return u.T <= 8 ? launch_pair<BITS, G, 1, 1>(u, d, st)
-                      : launch_pair<BITS, G, 1, 4>(u, d, st);
-    return u.T <= 8 ? launch_pair<BITS, G, 2, 1>(u, d, st)
-                    : launch_pair<BITS, G, 2, 4>(u, d, st);
+    switch (a.yt) {
+      case TTQ_BF16: return launch_mode<BITS, G, kOne>(a, st);
+      case TTQ_F16: return launch_mode<BITS, G, kTwo>(a, st);
+      case TTQ_F32: return launch_mode<BITS, G, kExact>(a, st);
+    }
+    return TTQ_ERR_INVALID_ARG;
   };
-  return u.group == 16 ? go(std::true_type{}) : go(std::false_type{});
+  return a.group == 16 ? go(std::true_type{}) : go(std::false_type{});
 }
 
 }  // namespace moe
