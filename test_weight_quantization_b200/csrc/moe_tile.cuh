@@ -47,17 +47,18 @@ constexpr int kChunk = 128;    // channels of one stage
 template <int BITS>
 constexpr int kPitch = 16 * (BITS | 1);
 template <int BITS>
-constexpr int kStageCodes = kRows * kPitch<BITS>;
-// delta (8 groups of 16 at most) and zero of the stage's rows
-constexpr int kStageDelta = kRows * 32;
-constexpr int kStageZero = kRows * 8;
-template <int BITS, bool G16>
-constexpr int kStage =
-    kStageCodes<BITS> + (G16 ? kStageDelta + kStageZero
-                             : kRows * 16 + kRows * 4);
-// Stages per warp: what lets two CTAs of 8 warps share an SM.
+constexpr int kStage = kRows * kPitch<BITS>;
+// delta and zero of the rows for 4 groups (8 of 16 channels): a piece
+template <bool G16>
+constexpr int kPieceDelta = G16 ? 32 : 16;
+template <bool G16>
+constexpr int kPiece = kRows * (kPieceDelta<G16> + kPieceDelta<G16> / 4);
+// Stages per warp: what lets two CTAs of 8 warps share an SM. As many pieces:
+// a stage needs at most one new one.
 template <int BITS>
 constexpr int kStages = BITS <= 3 ? 5 : BITS <= 5 ? 3 : 2;
+template <int BITS, bool G16>
+constexpr int kRing = kStages<BITS> * (kStage<BITS> + kPiece<G16>);
 
 // ------------------------------------------------------------- columns ---
 
@@ -202,7 +203,18 @@ struct Packed {
   const uint8_t* zero;
   int ldc, ldg;   // words, entries
   int blocks;
-  int group;
+  int lg;         // blocks per group = 1 << lg (groups of 32, 64, 128)
+
+  __device__ __forceinline__ Packed(const uint32_t* codes_,
+                                    const float* delta_, const uint8_t* zero_,
+                                    int K, int bits, int group)
+      : codes(codes_), delta(delta_), zero(zero_),
+        ldc((int)codes_ld(K, bits)), ldg((int)groups_ld(K, group)),
+        blocks(K / 32), lg(group == 128 ? 2 : group == 64 ? 1 : 0) {}
+  // Whether chunk c starts a piece of 4 groups (for groups of 16, 8: always).
+  __device__ __forceinline__ bool new_piece(int c) const {
+    return (c & ((1 << lg) - 1)) == 0;
+  }
 };
 
 // A lane's share of the copies of 32 rows: the tile's rows 0..15 are
@@ -216,8 +228,11 @@ struct Stream {
   const float* delta;       // of the lane's row
   const uint8_t* zero;
   int c;                    // the next chunk
+  int stage, piece;         // ring positions of the next copies
+  bool fresh;               // the next chunk is the tile's first
 
-  __device__ __forceinline__ Stream(const Packed& m, int skip, int lane) {
+  __device__ __forceinline__ Stream(const Packed& m, int skip, int lane)
+      : stage(0), piece(0), fresh(true) {
 #pragma unroll
     for (int i = 0; i < BITS; ++i) {
       const int p = lane + 32 * i, r = p / BITS;
@@ -235,10 +250,12 @@ struct Stream {
     delta = m.delta + row * m.ldg + row_off;
     zero = m.zero + row * m.ldg + row_off;
     c = c0;
+    fresh = true;
   }
   // Issues the copies of the next chunk and moves on.
-  __device__ __forceinline__ void copy(const Packed& m, uint32_t dst,
+  __device__ __forceinline__ void copy(const Packed& m, uint32_t ring,
                                        int lane) {
+    const uint32_t dst = ring + stage * kStage<BITS>;
     const int left = m.ldc - c * (4 * BITS);  // words of the row from here
     if (left >= 4 * BITS) {
 #pragma unroll
@@ -256,46 +273,35 @@ struct Stream {
                       codes + code_off[i]);
       }
     }
-    // the pitch of delta and zero is a multiple of 16 entries: a chunk's are
-    // always there
-    const uint32_t dd = dst + kStageCodes<BITS>;
-    if constexpr (G16) {
-      cp_async_16(dd + lane * 32, delta + c * 8);
-      cp_async_16(dd + lane * 32 + 16, delta + c * 8 + 4);
-      cp_async_ca<8>(dd + kStageDelta + lane * 8, zero + c * 8);
-    } else {
-      int g0 = c;
-      if (m.group == 32) {
-        g0 = c * 4;
-        cp_async_16(dd + lane * 16, delta + g0);
-      } else if (m.group == 64) {
-        g0 = c * 2;
-        cp_async_ca<8>(dd + lane * 16, delta + g0);
+    // The pitch of delta and zero is a multiple of 16 entries: a piece is
+    // always there.
+    if (fresh || m.new_piece(c)) {
+      constexpr int S = kStages<BITS>, kD = kPieceDelta<G16>;
+      const uint32_t dd = ring + S * kStage<BITS> + piece * kPiece<G16>;
+      if constexpr (G16) {
+        cp_async_16(dd + lane * kD, delta + c * 8);
+        cp_async_16(dd + lane * kD + 16, delta + c * 8 + 4);
+        cp_async_ca<8>(dd + kRows * kD + lane * 8, zero + c * 8);
       } else {
-        cp_async_ca<4>(dd + lane * 16, delta + g0);
+        const int q = (c >> m.lg) * 4;
+        cp_async_16(dd + lane * kD, delta + q);
+        cp_async_ca<4>(dd + kRows * kD + lane * 4, zero + q);
       }
-      // the aligned word that holds the chunk's zero points
-      cp_async_ca<4>(dd + kRows * 16 + lane * 4, zero + (g0 & ~3));
+      piece = piece + 1 == S ? 0 : piece + 1;
+      fresh = false;
     }
     codes += 16 * BITS;
     ++c;
+  }
+  __device__ __forceinline__ void advance() {
+    stage = stage + 1 == kStages<BITS> ? 0 : stage + 1;
   }
 };
 
 // ----------------------------------------------------------- unpacking ---
 
-__device__ __forceinline__ uint32_t lds32(uint32_t a) {
-  uint32_t v;
-  asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(a));
-  return v;
-}
-__device__ __forceinline__ uint32_t lds8(uint32_t a) {
-  uint32_t v;
-  asm volatile("ld.shared.u8 %0, [%1];" : "=r"(v) : "r"(a));
-  return v;
-}
-__device__ __forceinline__ float ldsf(uint32_t a) {
-  return __uint_as_float(lds32(a));
+__device__ __forceinline__ uint32_t word(const uint8_t* p) {
+  return *reinterpret_cast<const uint32_t*>(p);
 }
 
 template <int BITS>
@@ -342,13 +348,14 @@ struct Field {
     return pair_at<BITS, G16, NORM, I, FROM>(m);
   }
   // p[0], p[1] feed the block's first MMA, p[2], p[3] its second.
-  __device__ __forceinline__ void codes(uint32_t at, uint32_t (&p)[4]) const {
+  __device__ __forceinline__ void codes(const uint8_t* at,
+                                        uint32_t (&p)[4]) const {
     if constexpr (G16) {
       // pairs (0, 2), (1, 3) of each half's four codes
-      uint32_t u = lds32(at + w0), v = lds32(at + w2);
+      uint32_t u = word(at + w0), v = word(at + w2);
       if constexpr (BITS != 8) {
-        u = __funnelshift_r(u, lds32(at + w1), sh);
-        v = __funnelshift_r(v, lds32(at + w3), sh2);
+        u = __funnelshift_r(u, word(at + w1), sh);
+        v = __funnelshift_r(v, word(at + w3), sh2);
       }
       const uint32_t m = __byte_perm(u, u >> (2 * BITS), 0x5410);
       const uint32_t n = __byte_perm(v, v >> (2 * BITS), 0x5410);
@@ -360,21 +367,21 @@ struct Field {
       // u: codes 0..3, v: codes 4..7 from bit 0 on; pairs (i, i + 4)
       uint32_t u, v;
       if constexpr (BITS == 2) {
-        u = lds32(at + w0) >> sh;
+        u = word(at + w0) >> sh;
         v = u >> 8;
       } else if constexpr (BITS == 3) {
-        u = __funnelshift_r(lds32(at + w0), lds32(at + w1), sh);
+        u = __funnelshift_r(word(at + w0), word(at + w1), sh);
         v = u >> 12;
       } else if constexpr (BITS == 4) {
-        u = lds32(at + w0);
+        u = word(at + w0);
         v = u >> 16;
       } else if constexpr (BITS == 8) {
-        u = lds32(at + w0);
-        v = lds32(at + w1);
+        u = word(at + w0);
+        v = word(at + w1);
       } else {
-        const uint32_t a = lds32(at + w0), b = lds32(at + w1);
+        const uint32_t a = word(at + w0), b = word(at + w1);
         u = __funnelshift_r(a, b, sh);
-        const uint32_t hi = BITS == 7 ? __funnelshift_r(b, lds32(at + w2), sh)
+        const uint32_t hi = BITS == 7 ? __funnelshift_r(b, word(at + w2), sh)
                                       : b >> sh;
         v = __funnelshift_r(u, hi, 4 * BITS);
       }
@@ -439,35 +446,42 @@ __host__ __device__ constexpr uint32_t ones(int i) {
          << 26;
 }
 
-// One stage's products into acc[row tile][column tile]. xp[n] (and xp[n] +
-// term for the second term) points at the lane's activations of the stage: 16
-// bytes per 32-channel block, 64 bytes apart, .x and .y for the block's first
-// MMA, .z and .w for its second.
-template <int BITS, bool G16, int MODE, int NT, int NTMAX>
+// One stage's products into acc[row tile][column tile]. st: the stage's codes,
+// dd: its piece of delta and zero, j0: the stage's first group in it. LG: as
+// Packed::lg. FULL: the stage has 4 blocks (no branch then keeps the blocks'
+// instructions apart), otherwise nblocks. xp[n] (and xp[n] + term for the
+// second term) points at the lane's activations of the stage: 16 bytes per
+// 32-channel block, 64 bytes apart, .x and .y for the block's first MMA, .z
+// and .w for its second; xv holds the first block's.
+template <int BITS, bool G16, int LG, bool FULL, int MODE, int NT, int NTMAX>
 __device__ __forceinline__ void stage_products(
-    uint32_t st, const Field<BITS, G16, MODE == kExact>& f, int group, int c,
-    int nblocks, const uint4* const (&xp)[NTMAX], int64_t term,
+    const uint8_t* st, const uint8_t* dd, int j0,
+    const Field<BITS, G16, MODE == kExact>& f, int nblocks,
+    const uint4* const (&xp)[NTMAX], int64_t term,
     uint4 (&xv)[NTMAX][kTerms<MODE>], float (&acc)[2][NTMAX][4], int lane) {
   constexpr int TERMS = kTerms<MODE>;
   constexpr bool kCentre = MODE == kExact;
+  constexpr int kD = kPieceDelta<G16>;
   const int g = lane >> 2;
-  const uint32_t dd = st + kStageCodes<BITS>;
+  st += g * kPitch<BITS>;
+  const uint8_t* dp = dd + g * kD + j0 * 4;
+  const uint8_t* zp = dd + kRows * kD + g * (kD / 4) + j0;
   float cc[2][NT][4], s[NT][4];
   __half2 zc[2][2];
-  auto zero_at = [&](int r, int j) -> uint32_t {
-    if constexpr (G16) return lds8(dd + kStageDelta + r * 8 + j);
-    return lds8(dd + kRows * 16 + r * 4 + ((c * (kChunk / group) + j) & 3));
+  // row i * 8 + g of the tile, group j of the stage
+  auto zero_at = [&](int i, int j) -> uint32_t {
+    return zp[i * 8 * (kD / 4) + j];
+  };
+  auto delta_at = [&](int i, int j) -> float {
+    return __uint_as_float(word(dp + i * 8 * kD + j * 4));
   };
   auto centre = [&](int j) {
     if constexpr (kCentre) {
 #pragma unroll
-      for (int rt = 0; rt < 2; ++rt)
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const uint32_t z =
-              (0x6400u | zero_at(rt * 16 + g + 8 * i, j)) * 0x10001u;
-          zc[rt][i] = *reinterpret_cast<const __half2*>(&z);
-        }
+      for (int i = 0; i < 4; ++i) {
+        const uint32_t z = (0x6400u | zero_at(i, j)) * 0x10001u;
+        zc[i >> 1][i & 1] = *reinterpret_cast<const __half2*>(&z);
+      }
     }
   };
   auto clear = [&]() {
@@ -477,23 +491,20 @@ __device__ __forceinline__ void stage_products(
       for (int i = 0; i < 4; ++i) cc[0][n][i] = cc[1][n][i] = s[n][i] = 0.f;
   };
   // -z in units: 2^23 + z by one OR, and one exact fused multiply-add
-  auto minus_z = [&](int r, int j) -> float {
+  auto minus_z = [&](int i, int j) -> float {
     constexpr float u = kUnit<BITS, G16, MODE>;
-    return fmaf(__uint_as_float(0x4B000000u | zero_at(r, j)), -u,
+    return fmaf(__uint_as_float(0x4B000000u | zero_at(i, j)), -u,
                 8388608.f * u);
   };
   // acc += D (c - z s) for group j of the stage
   auto flush = [&](int j) {
 #pragma unroll
     for (int rt = 0; rt < 2; ++rt) {
-      const int r = rt * 16 + g;
-      constexpr int pitch = G16 ? 32 : 16;
-      const float d0 = ldsf(dd + r * pitch + j * 4);
-      const float d1 = ldsf(dd + (r + 8) * pitch + j * 4);
+      const float d0 = delta_at(2 * rt, j), d1 = delta_at(2 * rt + 1, j);
       float z0 = 0.f, z1 = 0.f;
       if constexpr (!kCentre) {
-        z0 = minus_z(r, j);
-        z1 = minus_z(r + 8, j);
+        z0 = minus_z(2 * rt, j);
+        z1 = minus_z(2 * rt + 1, j);
       }
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
@@ -522,24 +533,25 @@ __device__ __forceinline__ void stage_products(
     }
   };
   clear();
-  const int bpg = G16 ? 1 : group >> 5;  // blocks per group
 #pragma unroll
   for (int b = 0; b < 4; ++b) {
-    if (b < nblocks) {
-      // the next block's activations
+    if (FULL || b < nblocks) {
+      // the next block's activations, where they fit the registers
+      constexpr bool kAhead = NT * TERMS <= 2;
       uint4 xn[NT][TERMS];
 #pragma unroll
       for (int n = 0; n < NT; ++n)
 #pragma unroll
-        for (int k = 0; k < TERMS; ++k)
-          if (b < 3 && b + 1 < nblocks)
+        for (int k = 0; k < TERMS; ++k) {
+          if (kAhead && b < 3 && (FULL || b + 1 < nblocks))
             xn[n][k] = xp[n][k * term + (b + 1) * 4];
+          if (!kAhead && b > 0) xv[n][k] = xp[n][k * term + b * 4];
+        }
       uint32_t p[2][2][4];  // [row tile][row g, row g + 8][pair]
-      if (!G16 && b % bpg == 0) centre(b / bpg);
+      if (!G16 && (b & ((1 << LG) - 1)) == 0) centre(b >> LG);
 #pragma unroll
       for (int rt = 0; rt < 2; ++rt) {
-        const uint32_t at =
-            st + (rt * 16 + g) * kPitch<BITS> + b * (4 * BITS);
+        const uint8_t* at = st + rt * 16 * kPitch<BITS> + b * (4 * BITS);
         f.codes(at, p[rt][0]);
         f.codes(at + 8 * kPitch<BITS>, p[rt][1]);
         if constexpr (kCentre && !G16) {
@@ -576,15 +588,16 @@ __device__ __forceinline__ void stage_products(
             for (int k = 0; k < TERMS; ++k)
               products(p, h, n, h ? xv[n][k].z : xv[n][k].x,
                        h ? xv[n][k].w : xv[n][k].y);
-        if ((b + 1) % bpg == 0) {
-          flush(b / bpg);
+        if (((b + 1) & ((1 << LG) - 1)) == 0) {
+          flush(b >> LG);
           if (b < 3) clear();
         }
       }
 #pragma unroll
       for (int n = 0; n < NT; ++n)
 #pragma unroll
-        for (int k = 0; k < TERMS; ++k) xv[n][k] = xn[n][k];
+        for (int k = 0; k < TERMS; ++k)
+          if (kAhead && b < 3) xv[n][k] = xn[n][k];
     }
   }
 }
@@ -618,26 +631,32 @@ __device__ __forceinline__ float row_unscale(uint32_t max_bits, int most) {
   return __uint_as_float((uint32_t)(127 - row_exponent(max_bits, most)) << 23);
 }
 
-// One warp's walk through its stages: x rows, products.
+// One warp's walk through its stages: activation rows, products.
 template <int BITS, bool G16, int MODE, int NTMAX>
 struct Tile {
   static constexpr int TERMS = kTerms<MODE>;
-  static constexpr int S = kStages<BITS>, kSt = kStage<BITS, G16>;
+  static constexpr int S = kStages<BITS>;
   const Field<BITS, G16, MODE == kExact> f;
-  uint32_t ring;
+  const uint8_t* ring;
   int lane, nt;
+  int stage, piece;        // ring positions: of the next stage, after the last
+                           // piece
+  bool fresh;
   const uint4* xp[NTMAX];  // the lane's activations at the next stage
   int64_t term;
   float acc[2][NTMAX][4];
 
-  __device__ __forceinline__ Tile(uint32_t ring_, int lane_, int64_t term_)
-      : f(lane_ & 3), ring(ring_), lane(lane_), term(term_) {}
+  __device__ __forceinline__ Tile(const uint8_t* ring_, int lane_,
+                                  int64_t term_)
+      : f(lane_ & 3), ring(ring_), lane(lane_), stage(0), piece(0),
+        term(term_) {}
 
   // Starts a tile with `cols` columns; row(col) gives a column's activations
   // (columns past the last repeat column 0: their results are dropped).
   template <typename RF>
   __device__ __forceinline__ void start(int cols, int c, RF&& row) {
     nt = (cols + 7) / 8;
+    fresh = true;
 #pragma unroll
     for (int n = 0; n < NTMAX; ++n) {
 #pragma unroll
@@ -646,35 +665,46 @@ struct Tile {
       xp[n] = row(col < cols ? col : 0) + c * 16 + (lane & 3);
     }
   }
-  template <int NT>
-  __device__ __forceinline__ void fetch(uint4 (&xv)[NTMAX][TERMS]) {
+  // Chunks c .. c_end - 1; next() issues the copies that refill the ring.
+  template <int LG, int NT, typename NF>
+  __device__ __forceinline__ void run_nt(const Packed& m, int c, int c_end,
+                                         NF&& next) {
+    for (; c < c_end; ++c) {
+      uint4 xv[NTMAX][TERMS];
 #pragma unroll
-    for (int n = 0; n < NT; ++n)
+      for (int n = 0; n < NT; ++n)
 #pragma unroll
-      for (int k = 0; k < TERMS; ++k) xv[n][k] = xp[n][k * term];
+        for (int k = 0; k < TERMS; ++k) xv[n][k] = xp[n][k * term];
+      cp_async_wait<S - 2>();
+      __syncwarp();  // the stage is there, and every lane has left the last
+      next();
+      if (fresh || m.new_piece(c)) {
+        piece = piece + 1 == S ? 0 : piece + 1;
+        fresh = false;
+      }
+      const uint8_t* st = ring + stage * kStage<BITS>;
+      const uint8_t* dd = ring + S * kStage<BITS> +
+                          (piece == 0 ? S - 1 : piece - 1) * kPiece<G16>;
+      const int j0 = G16 ? 0 : (c * (4 >> LG)) & 3;
+      const int nb = m.blocks - 4 * c;
+      if (nb >= 4)
+        stage_products<BITS, G16, LG, true, MODE, NT, NTMAX>(
+            st, dd, j0, f, 4, xp, term, xv, acc, lane);
+      else
+        stage_products<BITS, G16, LG, false, MODE, NT, NTMAX>(
+            st, dd, j0, f, nb, xp, term, xv, acc, lane);
+#pragma unroll
+      for (int n = 0; n < NT; ++n) xp[n] += 16;
+      stage = stage + 1 == S ? 0 : stage + 1;
+    }
   }
-  // One stage; next() issues the copies that refill the ring.
-  template <int NT, typename NF>
-  __device__ __forceinline__ void step_nt(const Packed& m, int c, int slot,
-                                          NF&& next) {
-    uint4 xv[NTMAX][TERMS];
-    fetch<NT>(xv);
-    cp_async_wait<S - 2>();
-    __syncwarp();  // the stage is there, and every lane has left the last one
-    next();
-    stage_products<BITS, G16, MODE, NT, NTMAX>(
-        ring + slot * kSt, f, m.group, c, min(4, m.blocks - 4 * c), xp, term,
-        xv, acc, lane);
-#pragma unroll
-    for (int n = 0; n < NT; ++n) xp[n] += 16;
-  }
-  template <typename NF>
-  __device__ __forceinline__ void step(const Packed& m, int c, int slot,
-                                       NF&& next) {
+  template <int LG, typename NF>
+  __device__ __forceinline__ void run(const Packed& m, int c, int c_end,
+                                      NF&& next) {
     if (NTMAX == 1 || nt == 1)
-      step_nt<1>(m, c, slot, next);
+      run_nt<LG, 1>(m, c, c_end, next);
     else
-      step_nt<NTMAX>(m, c, slot, next);
+      run_nt<LG, NTMAX>(m, c, c_end, next);
   }
 };
 
@@ -686,18 +716,20 @@ struct Tile {
 // of K; units (entry, rs tiles) are taken round robin by a persistent grid.
 // Neighbouring tiles share their activations through L1; parts of K are added
 // through shared memory.
-template <int BITS, bool G16, int MODE, int NTMAX>
+template <int BITS, bool G16, int LG, int MODE, int NTMAX>
 __global__ void __launch_bounds__(kThreads, 2)
     up_kernel(const UpArgs a) {
   using TileT = Tile<BITS, G16, MODE, NTMAX>;
-  constexpr int S = TileT::S, kSt = TileT::kSt;
+  constexpr int S = TileT::S;
   extern __shared__ __align__(16) uint8_t sm[];
   Lists l(sm, a.T * a.top_k, a.E);
   float* red =  // [warp][row tile][column tile][128]
       reinterpret_cast<float*>(sm + Lists::bytes(a.T * a.top_k, a.E));
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const uint32_t ring =
-      smem_u32(red) + kWarps * 2 * NTMAX * 128 * 4 + warp * S * kSt;
+  const uint8_t* ring = reinterpret_cast<const uint8_t*>(
+                            red + kWarps * 2 * NTMAX * 128) +
+                        warp * kRing<BITS, G16>;
+  const uint32_t ring_at = smem_u32(ring);
 
   // ids and the packed weights were complete before the kernel that runs
   // before this one started: lists and the first stages need not wait for it
@@ -708,18 +740,11 @@ __global__ void __launch_bounds__(kThreads, 2)
   const int units = l.entries * rows;
   const int chunks = (a.K + kChunk - 1) / kChunk;
   const int c0 = wk * chunks / ks, c1 = (wk + 1) * chunks / ks;
-  Packed m;
-  m.codes = a.codes;
-  m.delta = a.delta;
-  m.zero = a.zero;
-  m.ldc = (int)codes_ld(a.K, BITS);
-  m.ldg = (int)groups_ld(a.K, a.group);
-  m.blocks = a.K / 32;
-  m.group = a.group;
+  const Packed m(a.codes, a.delta, a.zero, a.K, BITS, a.group);
   Stream<BITS, G16> w(m, a.I, lane);
 
   // the warp's stages: its chunks of the CTA's units, one after the other
-  int iu = blockIdx.x, ist = 0;
+  int iu = blockIdx.x;
   auto seek = [&]() {
     // the warp's tile of unit iu, skipping units in which it has none
     for (; iu < units && c0 < c1; iu += gridDim.x) {
@@ -733,14 +758,14 @@ __global__ void __launch_bounds__(kThreads, 2)
   };
   auto issue = [&]() {
     if (iu < units) {
-      w.copy(m, ring + ist * kSt, lane);
+      w.copy(m, ring_at, lane);
       if (w.c == c1) {
         iu += gridDim.x;
         seek();
       }
     }
     cp_async_commit();
-    ist = ist + 1 == S ? 0 : ist + 1;
+    w.advance();
   };
   seek();
 #pragma unroll
@@ -748,7 +773,6 @@ __global__ void __launch_bounds__(kThreads, 2)
   griddep_enter();
 
   TileT tl(ring, lane, (int64_t)a.T * a.K / 8);
-  int cst = 0;
   for (int u = blockIdx.x; u < units; u += gridDim.x) {
     const int en = u / rows, tile = (u - en * rows) * rs + wr;
     const int cols = l.cols[en], col0 = l.first[en];
@@ -756,12 +780,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     tl.start(cols, c0, [&](int col) {
       return a.xhat + (int64_t)(l.slot[col0 + col] / a.top_k) * (a.K / 8);
     });
-    if (live) {
-      for (int c = c0; c < c1; ++c) {
-        tl.step(m, c, cst, issue);
-        cst = cst + 1 == S ? 0 : cst + 1;
-      }
-    }
+    if (live) tl.template run<LG>(m, c0, c1, issue);
     if (ks > 1) {
       // parts of K to the warp of part 0
       __syncthreads();  // the last sums have been read
@@ -828,18 +847,21 @@ __global__ void __launch_bounds__(kThreads, 2)
 // are one list, split evenly over the parts of all CTAs of a cluster. Every
 // warp keeps the sums of all tokens for its share and adds an entry's columns
 // to them when it leaves the entry; parts are added at the end, in order.
-template <int BITS, bool G16, int MODE, int NTMAX>
+template <int BITS, bool G16, int LG, int MODE, int NTMAX>
 __global__ void __launch_bounds__(kThreads, 2)
     down_kernel(const DownArgs a) {
   using TileT = Tile<BITS, G16, MODE, NTMAX>;
-  constexpr int S = TileT::S, kSt = TileT::kSt;
+  constexpr int S = TileT::S;
   extern __shared__ __align__(16) uint8_t sm[];
   Lists l(sm, a.T * a.top_k, a.E);
   float* ysum =  // [warp][T][32]
       reinterpret_cast<float*>(sm + Lists::bytes(a.T * a.top_k, a.E));
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int region = a.T * kRows;
-  const uint32_t ring = smem_u32(ysum + kWarps * region) + warp * S * kSt;
+  const uint8_t* ring =
+      reinterpret_cast<const uint8_t*>(ysum + kWarps * region) +
+      warp * kRing<BITS, G16>;
+  const uint32_t ring_at = smem_u32(ring);
   float* mine = ysum + warp * region;
 
   // as in up_kernel: nothing before griddep_enter() reads what the kernel
@@ -855,30 +877,23 @@ __global__ void __launch_bounds__(kThreads, 2)
   const int parts = ranks * ks, part = rank * ks + wk;
   const int s0 = (int)((int64_t)total * part / parts);
   const int s1 = (int)((int64_t)total * (part + 1) / parts);
-  Packed m;
-  m.codes = a.codes;
-  m.delta = a.delta;
-  m.zero = a.zero;
-  m.ldc = (int)codes_ld(a.I, BITS);
-  m.ldg = (int)groups_ld(a.I, a.group);
-  m.blocks = a.I / 32;
-  m.group = a.group;
+  const Packed m(a.codes, a.delta, a.zero, a.I, BITS, a.group);
   Stream<BITS, G16> w(m, 16, lane);
-  int is = s0, ien = s0 / chunks, ist = 0;
+  int is = s0, ien = s0 / chunks;
   auto seek = [&](int c) {
     w.seek(m, (int64_t)l.expert[ien] * a.K + tile * kRows, c);
   };
   if (s0 < s1) seek(s0 - ien * chunks);
   auto issue = [&]() {
     if (is < s1) {
-      w.copy(m, ring + ist * kSt, lane);
+      w.copy(m, ring_at, lane);
       if (++is < s1 && w.c == chunks) {
         ++ien;
         seek(0);
       }
     }
     cp_async_commit();
-    ist = ist + 1 == S ? 0 : ist + 1;
+    w.advance();
   };
 #pragma unroll
   for (int i = 0; i < S - 1; ++i) issue();
@@ -886,17 +901,15 @@ __global__ void __launch_bounds__(kThreads, 2)
 
   const int t = lane & 3, g = lane >> 2;
   TileT tl(ring, lane, (int64_t)a.T * a.top_k * a.I / 8);
-  int s = s0, en = s0 / chunks, c = s0 - en * chunks, cst = 0;
+  int s = s0, en = s0 / chunks, c = s0 - en * chunks;
   while (s < s1) {
     const int cols = l.cols[en], col0 = l.first[en];
     tl.start(cols, c, [&](int col) {
       return a.hhat + (int64_t)l.slot[col0 + col] * (a.I / 8);
     });
     const int stop = min(s1, s + chunks - c);
-    for (; s < stop; ++s, ++c) {
-      tl.step(m, c, cst, issue);
-      cst = cst + 1 == S ? 0 : cst + 1;
-    }
+    tl.template run<LG>(m, c, c + stop - s, issue);
+    s = stop;
     // leave the entry: its columns are different tokens
     constexpr float per_unit = 1.f / kUnit<BITS, G16, MODE>;
     constexpr int most = MODE == kExact ? 0 : Positions<BITS, G16>::kMost;
@@ -964,12 +977,12 @@ __global__ void __launch_bounds__(kThreads, 2)
 template <int BITS, bool G16>
 size_t up_smem(int ntmax, int n, int E) {
   return Lists::bytes(n, E) + (size_t)kWarps * 2 * ntmax * 128 * 4 +
-         (size_t)kWarps * kStages<BITS> * kStage<BITS, G16>;
+         (size_t)kWarps * kRing<BITS, G16>;
 }
 template <int BITS, bool G16>
 size_t down_smem(int T, int n, int E) {
   return Lists::bytes(n, E) + (size_t)kWarps * T * kRows * 4 +
-         (size_t)kWarps * kStages<BITS> * kStage<BITS, G16>;
+         (size_t)kWarps * kRing<BITS, G16>;
 }
 
 template <typename K>
@@ -997,7 +1010,7 @@ inline int pick_rs(int64_t tiles, int64_t slots) {
 
 inline int ctas_per_sm(size_t smem) { return smem + 1024 <= 114 * 1024 ? 2 : 1; }
 
-template <int BITS, bool G16, int MODE, int NTMAX>
+template <int BITS, bool G16, int LG, int MODE, int NTMAX>
 ttq_status launch_up(UpArgs u, cudaStream_t st) {
   LaunchShape ls;
   ls.block = dim3(kThreads);
@@ -1007,12 +1020,12 @@ ttq_status launch_up(UpArgs u, cudaStream_t st) {
       (int64_t)Lists::max_entries(u.T * u.top_k, u.E) * (u.I / 16);
   u.rs = pick_rs(tiles, slots);
   ls.grid = dim3((unsigned)std::min<int64_t>(tiles, slots));
-  auto kern = up_kernel<BITS, G16, MODE, NTMAX>;
+  auto kern = up_kernel<BITS, G16, LG, MODE, NTMAX>;
   if (!allow_smem(kern, ls.smem)) return TTQ_ERR_CUDA;
   return launch(ls, st, kern, u);
 }
 
-template <int BITS, bool G16, int MODE, int NTMAX>
+template <int BITS, bool G16, int LG, int MODE, int NTMAX>
 ttq_status launch_down(DownArgs d, cudaStream_t st) {
   LaunchShape ls;
   ls.block = dim3(kThreads);
@@ -1026,7 +1039,7 @@ ttq_status launch_down(DownArgs d, cudaStream_t st) {
   const int ranks = std::max(1, std::min(8, slots / grid));
   ls.grid = dim3((unsigned)grid, (unsigned)ranks);
   ls.cluster_y = (unsigned)ranks;
-  auto kern = down_kernel<BITS, G16, MODE, NTMAX>;
+  auto kern = down_kernel<BITS, G16, LG, MODE, NTMAX>;
   if (!allow_smem(kern, ls.smem)) return TTQ_ERR_CUDA;
   return launch(ls, st, kern, d);
 }
@@ -1034,29 +1047,36 @@ ttq_status launch_down(DownArgs d, cudaStream_t st) {
 // NTMAX: up to 8 tokens fill one column tile; more may put up to 16 on one
 // entry. (Four tiles did not fit the registers of two CTAs per SM: an expert
 // with more than 16 tokens becomes two entries, the second read from L2.)
-template <int BITS, bool G16, int MODE>
+template <int BITS, bool G16, int LG, int MODE>
 ttq_status launch_mode(const UpArgs& u, cudaStream_t st) {
-  return u.T <= 8 ? launch_up<BITS, G16, MODE, 1>(u, st)
-                  : launch_up<BITS, G16, MODE, 2>(u, st);
+  return u.T <= 8 ? launch_up<BITS, G16, LG, MODE, 1>(u, st)
+                  : launch_up<BITS, G16, LG, MODE, 2>(u, st);
 }
-template <int BITS, bool G16, int MODE>
+template <int BITS, bool G16, int LG, int MODE>
 ttq_status launch_mode(const DownArgs& d, cudaStream_t st) {
-  return d.T <= 8 ? launch_down<BITS, G16, MODE, 1>(d, st)
-                  : launch_down<BITS, G16, MODE, 2>(d, st);
+  return d.T <= 8 ? launch_down<BITS, G16, LG, MODE, 1>(d, st)
+                  : launch_down<BITS, G16, LG, MODE, 2>(d, st);
+}
+
+template <int BITS, bool G16, int LG, typename Args>
+ttq_status launch_group(const Args& a, cudaStream_t st) {
+  switch (a.yt) {
+    case TTQ_BF16: return launch_mode<BITS, G16, LG, kOne>(a, st);
+    case TTQ_F16: return launch_mode<BITS, G16, LG, kTwo>(a, st);
+    case TTQ_F32: return launch_mode<BITS, G16, LG, kExact>(a, st);
+  }
+  return TTQ_ERR_INVALID_ARG;
 }
 
 template <int BITS, typename Args>
 ttq_status launch_bits(const Args& a, cudaStream_t st) {
-  auto go = [&](auto g16) -> ttq_status {
-    constexpr bool G = decltype(g16)::value;
-    switch (a.yt) {
-      case TTQ_BF16: return launch_mode<BITS, G, kOne>(a, st);
-      case TTQ_F16: return launch_mode<BITS, G, kTwo>(a, st);
-      case TTQ_F32: return launch_mode<BITS, G, kExact>(a, st);
-    }
-    return TTQ_ERR_INVALID_ARG;
-  };
-  return a.group == 16 ? go(std::true_type{}) : go(std::false_type{});
+  switch (a.group) {
+    case 16: return launch_group<BITS, true, 0>(a, st);
+    case 32: return launch_group<BITS, false, 0>(a, st);
+    case 64: return launch_group<BITS, false, 1>(a, st);
+    case 128: return launch_group<BITS, false, 2>(a, st);
+  }
+  return TTQ_ERR_INVALID_ARG;
 }
 
 }  // namespace moe
