@@ -51,13 +51,14 @@ __device__ __forceinline__ uint32_t half2_bits(float a, float b) {
 // Row r = blockIdx.x of [rows, n 8-channel vectors], times inv_s unless that
 // is NULL, as fp16 terms xhat[term][row]: times 2^k, with k from the row's
 // largest value (row_exponent), and 2^(most - at) of the code pair each
-// channel meets. The first term rounds every value above 2^-27 of the largest
+// channel meets. sums[row]: the rounded values' sums over each group. The first term rounds every value above 2^-27 of the largest
 // to 11 bits, the second what is left.
 template <typename TX>
 __global__ void __launch_bounds__(kThreads)
     rows_kernel(const TX* X, int64_t ldx, const float* inv_s, int n,
                 int terms, bool g16, int4 up, int most, uint4* xhat,
-                uint32_t* xmax, const int32_t* ids, int E) {
+                float* sums, int ldg, int group, uint32_t* xmax,
+                const int32_t* ids, int E) {
   __shared__ uint32_t warp_max[kThreads / 32];
   griddep_enter();
   const int r = blockIdx.x;
@@ -74,7 +75,7 @@ __global__ void __launch_bounds__(kThreads)
     }
   };
   constexpr int kKeep = 2;  // vectors kept in registers between the passes
-  float kept[kKeep][8];
+  float kept[kKeep][8] = {};
   uint32_t mx = 0;
 #pragma unroll
   for (int j = 0; j < kKeep; ++j) {
@@ -104,7 +105,11 @@ __global__ void __launch_bounds__(kThreads)
   const float sc = __uint_as_float((uint32_t)(127 + k2) << 23);
   const float s0 = (float)(1 << up.x), s1 = (float)(1 << up.y),
               s2 = (float)(1 << up.z), s3 = (float)(1 << up.w);
+  // every lane of a warp calls store together: i < n or not, groups are
+  // whole lanes
   auto store = [&](int i, float (&v)[8]) {
+    const bool live = i < n;
+    float total = 0.f;
     if (g16) {
       // channels 4m..4m+3 of a half: lane m's pairs (0, 2), (1, 3)
       const float f0 = (i >> 1) & 1 ? s2 : s0, f1 = (i >> 1) & 1 ? s3 : s1;
@@ -119,6 +124,7 @@ __global__ void __launch_bounds__(kThreads)
     }
     for (int k = 0; k < terms; ++k) {
       uint4* out = xhat + ((int64_t)k * gridDim.x + r) * n;
+      const bool put = live;
       uint32_t p[4];
       float a[8];
       if (g16) {
@@ -128,8 +134,10 @@ __global__ void __launch_bounds__(kThreads)
         p[3] = half2_bits(v[5], v[7]);
         const int blk = i / 4, half = (i >> 1) & 1, m = 2 * (i & 1);
         uint2* o = reinterpret_cast<uint2*>(out + blk * 4);
-        o[m * 2 + half] = make_uint2(p[0], p[1]);
-        o[(m + 1) * 2 + half] = make_uint2(p[2], p[3]);
+        if (put) {
+          o[m * 2 + half] = make_uint2(p[0], p[1]);
+          o[(m + 1) * 2 + half] = make_uint2(p[2], p[3]);
+        }
         f16x2_to_f32(p[0], a[0], a[2]);
         f16x2_to_f32(p[1], a[1], a[3]);
         f16x2_to_f32(p[2], a[4], a[6]);
@@ -140,32 +148,52 @@ __global__ void __launch_bounds__(kThreads)
           p[q] = half2_bits(v[q], v[q + 4]);
           f16x2_to_f32(p[q], a[q], a[q + 4]);
         }
-        out[i] = make_uint4(p[0], p[1], p[2], p[3]);
+        if (put) out[i] = make_uint4(p[0], p[1], p[2], p[3]);
+      }
+      // back to the natural size: powers of two, exact
+      if (g16) {
+        const float f0 = (i >> 1) & 1 ? s2 : s0, f1 = (i >> 1) & 1 ? s3 : s1;
+#pragma unroll
+        for (int q = 0; q < 8; ++q) total += a[q] / (q & 1 ? f1 : f0);
+      } else {
+#pragma unroll
+        for (int q = 0; q < 8; ++q)
+          total += a[q] / ((q & 3) == 0   ? s0
+                           : (q & 3) == 1 ? s1
+                           : (q & 3) == 2 ? s2
+                                          : s3);
       }
 #pragma unroll
       for (int q = 0; q < 8; ++q) v[q] -= a[q];
     }
+    for (int o = group / 16; o > 0; o >>= 1)
+      total += __shfl_xor_sync(0xffffffffu, total, o);
+    if (live && i % (group / 8) == 0)
+      sums[(int64_t)r * ldg + i / (group / 8)] = total;
   };
 #pragma unroll
   for (int j = 0; j < kKeep; ++j) {
     const int i = threadIdx.x + j * kThreads;
-    if (i < n) store(i, kept[j]);
+    if (j * kThreads < n) store(i, kept[j]);
   }
-  for (int i = threadIdx.x + kKeep * kThreads; i < n; i += kThreads) {
-    float v[8];
-    load(i, v);
+  for (int base = kKeep * kThreads; base < n; base += kThreads) {
+    const int i = base + threadIdx.x;
+    float v[8] = {};
+    if (i < n) load(i, v);
     store(i, v);
   }
 }
 
-// Workspace: xhat and hhat (two terms each), h, xmax, hmax; every part a
-// multiple of 16 bytes.
+// Workspace: xhat and hhat (two terms each), h, xsum, hsum, xmax, hmax; every
+// part a multiple of 16 bytes. The sums are sized for groups of 16.
 struct Layout {
-  size_t hhat, h, xmax, hmax, bytes;
+  size_t hhat, h, xsum, hsum, xmax, hmax, bytes;
   Layout(int64_t T, int64_t K, int64_t I, int top_k) {
     hhat = (size_t)2 * T * K * 2;
     h = hhat + (size_t)2 * T * top_k * I * 2;
-    xmax = h + (size_t)T * top_k * I * 4;
+    xsum = h + (size_t)T * top_k * I * 4;
+    hsum = xsum + (size_t)T * groups_ld(K, 16) * 4;
+    xmax = hsum + (size_t)T * top_k * groups_ld(I, 16) * 4;
     hmax = xmax + (size_t)(T + 3) / 4 * 16;
     bytes = hmax + (size_t)(T * top_k + 3) / 4 * 16;
   }
@@ -197,6 +225,8 @@ ttq_status launch_moe_lowbit(const MoeArgs& a, cudaStream_t st) {
   uint4* xhat = reinterpret_cast<uint4*>(ws);
   uint4* hhat = reinterpret_cast<uint4*>(ws + l.hhat);
   float* h = reinterpret_cast<float*>(ws + l.h);
+  float* xsum = reinterpret_cast<float*>(ws + l.xsum);
+  float* hsum = reinterpret_cast<float*>(ws + l.hsum);
   uint32_t* xmax = reinterpret_cast<uint32_t*>(ws + l.xmax);
   uint32_t* hmax = reinterpret_cast<uint32_t*>(ws + l.hmax);
   const bool g16 = a.group == 16;
@@ -215,15 +245,17 @@ ttq_status launch_moe_lowbit(const MoeArgs& a, cudaStream_t st) {
   LaunchShape ls;
   ls.block = dim3(kThreads);
   auto rows = [&](auto* x, int64_t count, int64_t ld, int64_t width,
-                  const float* inv_s, uint4* hat, uint32_t* max,
+                  const float* inv_s, uint4* hat, float* sum, uint32_t* max,
                   const int32_t* ids) {
     using TX = std::remove_const_t<std::remove_pointer_t<decltype(x)>>;
     ls.grid = dim3((unsigned)count);
     return launch(ls, st, rows_kernel<TX>, x, ld, inv_s, (int)(width / 8),
-                  terms, g16, up, most, hat, max, ids, (int)a.E);
+                  terms, g16, up, most, hat, sum,
+                  (int)groups_ld(width, a.group), a.group, max, ids,
+                  (int)a.E);
   };
   auto x_rows = [&](auto* x) {
-    return rows(x, a.T, a.ldx, a.K, a.inv_s, xhat, xmax, nullptr);
+    return rows(x, a.T, a.ldx, a.K, a.inv_s, xhat, xsum, xmax, nullptr);
   };
   ttq_status s =
       a.xt == TTQ_F32    ? x_rows(static_cast<const float*>(a.X))
@@ -232,6 +264,7 @@ ttq_status launch_moe_lowbit(const MoeArgs& a, cudaStream_t st) {
   if (s != TTQ_OK) return s;
   moe::UpArgs u;
   u.xhat = xhat;
+  u.xsum = xsum;
   u.xmax = xmax;
   u.ids = a.ids;
   u.T = (int)a.T;
@@ -252,10 +285,11 @@ ttq_status launch_moe_lowbit(const MoeArgs& a, cudaStream_t st) {
   s = launch_width(a.bits, u, st);
   if (s != TTQ_OK) return s;
   s = rows(static_cast<const float*>(h), a.T * a.top_k, a.I, a.I, nullptr,
-           hhat, hmax, a.ids);
+           hhat, hsum, hmax, a.ids);
   if (s != TTQ_OK) return s;
   moe::DownArgs d;
   d.hhat = hhat;
+  d.hsum = hsum;
   d.hmax = hmax;
   d.ids = a.ids;
   d.weights = a.weights;

@@ -51,10 +51,12 @@ __host__ __device__ inline int row_exponent(uint32_t max_bits, int most) {
 }
 
 // xhat: fp16 terms of the rows, [term][T][K], in the order the code pairs
-// want; xmax: bits of a token's largest |x|; h [T top_k][I] fp32, and hhat,
-// hmax as xhat and xmax for its rows.
+// want; xsum [T][groups_ld]: the rows' sums over every group (times 2^k);
+// xmax: bits of a token's largest |x|. h [T top_k][I] fp32, and
+// hhat, hsum, hmax for its rows.
 struct UpArgs {
   const uint4* xhat;
+  const float* xsum;
   const uint32_t* xmax;
   const int32_t* ids;
   int T, K, I, E, top_k, group, act, rs;
@@ -68,6 +70,7 @@ struct UpArgs {
 };
 struct DownArgs {
   const uint4* hhat;
+  const float* hsum;
   const uint32_t* hmax;
   const int32_t* ids;
   const float* weights;

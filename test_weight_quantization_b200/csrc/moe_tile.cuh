@@ -13,9 +13,11 @@
 //     there is. Codes are used at several P without a shift; the activations
 //     that meet them carry 2^(Pmax-P) (Positions). Per group,
 //       acc += D (sum q x - z sum x),
-//     with sum x from one more MMA whose A undoes 2^(Pmax-P), in the same
-//     accumulator layout. D (fp32) and z are applied in fp32; 2^(24-Pmax) and
-//     the row's power of two return in the epilogue.
+//     with the groups' sums of x made once with the activations. (They came
+//     from one more MMA at first; a legacy m16n8k16 occupies its tensor pipe
+//     for 8 cycles, so that was a third of the pipe's time.) D (fp32) and z are
+//     applied in fp32; 2^(24-Pmax) and the row's power of two return in the
+//     epilogue.
 //   - The contraction order inside a 32-code block is free as long as both
 //     operands agree: lane t of a quad owns codes 8t..8t+7 (for groups of 16:
 //     4t..4t+3 of both halves), which are consecutive bits of one word (4
@@ -72,6 +74,7 @@ struct Lists {
   int* start;          // [E] the first column of an expert
   float* weight;       // [n] routing weight of a column
   uint16_t* slot;      // [n] the columns' slots, sorted by expert
+  uint8_t* token;      // [n] and their tokens
   int16_t* expert;     // [entries] of an entry: expert, first column, columns
   int16_t* first;
   int16_t* cols;
@@ -82,7 +85,7 @@ struct Lists {
     return (n < E ? n : E) + n / kMaxCols;
   }
   static __host__ __device__ size_t bytes(int n, int E) {
-    const size_t b = (size_t)E * 12 + (size_t)n * 6 +
+    const size_t b = (size_t)E * 12 + (size_t)n * 7 +
                      (size_t)max_entries(n, E) * 6 + (2 * kWarps + 1) * 4;
     return (b + 127) / 128 * 128;
   }
@@ -96,6 +99,7 @@ struct Lists {
     expert = reinterpret_cast<int16_t*>(slot + n);
     first = expert + m;
     cols = first + m;
+    token = reinterpret_cast<uint8_t*>(cols + m);
   }
 };
 
@@ -177,6 +181,7 @@ __device__ __forceinline__ void build_lists(Lists& l, const int32_t* ids,
                                         : __popc(m.x) + __popc(m.y & below));
     l.slot[at] = (uint16_t)p;
     l.weight[at] = w;
+    l.token[at] = (uint8_t)t;
   }
   __syncthreads();
 }
@@ -436,29 +441,22 @@ __device__ __forceinline__ void subtract(uint32_t& p, __half2 z) {
   p = *reinterpret_cast<const uint32_t*>(&d);
 }
 
-// 2^-(kMost - at(i)) in both halves: the weights of the sum of x.
-template <int BITS, bool G16>
-__host__ __device__ constexpr uint32_t ones(int i) {
-  return (uint32_t)(15 - (Positions<BITS, G16>::kMost -
-                          Positions<BITS, G16>::at(i)))
-         << 10 | (uint32_t)(15 - (Positions<BITS, G16>::kMost -
-                                  Positions<BITS, G16>::at(i)))
-         << 26;
-}
-
 // One stage's products into acc[row tile][column tile]. st: the stage's codes,
 // dd: its piece of delta and zero, j0: the stage's first group in it. LG: as
 // Packed::lg. FULL: the stage has 4 blocks (no branch then keeps the blocks'
 // instructions apart), otherwise nblocks. xp[n] (and xp[n] + term for the
 // second term) points at the lane's activations of the stage: 16 bytes per
 // 32-channel block, 64 bytes apart, .x and .y for the block's first MMA, .z
-// and .w for its second; xv holds the first block's.
+// and .w for its second; xv holds the first block's. sums[n] holds, in lane
+// (g, t), the sum of x of column g's group t of the piece (of 16-channel
+// groups: 2t and 2t + 1).
 template <int BITS, bool G16, int LG, bool FULL, int MODE, int NT, int NTMAX>
 __device__ __forceinline__ void stage_products(
     const uint8_t* st, const uint8_t* dd, int j0,
     const Field<BITS, G16, MODE == kExact>& f, int nblocks,
     const uint4* const (&xp)[NTMAX], int64_t term,
-    uint4 (&xv)[NTMAX][kTerms<MODE>], float (&acc)[2][NTMAX][4], int lane) {
+    uint4 (&xv)[NTMAX][kTerms<MODE>], const float2 (&sums)[NTMAX],
+    float (&acc)[2][NTMAX][4], int lane) {
   constexpr int TERMS = kTerms<MODE>;
   constexpr bool kCentre = MODE == kExact;
   constexpr int kD = kPieceDelta<G16>;
@@ -466,7 +464,7 @@ __device__ __forceinline__ void stage_products(
   st += g * kPitch<BITS>;
   const uint8_t* dp = dd + g * kD + j0 * 4;
   const uint8_t* zp = dd + kRows * kD + g * (kD / 4) + j0;
-  float cc[2][NT][4], s[NT][4];
+  float cc[2][NT][4];
   __half2 zc[2][2];
   // row i * 8 + g of the tile, group j of the stage
   auto zero_at = [&](int i, int j) -> uint32_t {
@@ -488,7 +486,7 @@ __device__ __forceinline__ void stage_products(
 #pragma unroll
     for (int n = 0; n < NT; ++n)
 #pragma unroll
-      for (int i = 0; i < 4; ++i) cc[0][n][i] = cc[1][n][i] = s[n][i] = 0.f;
+      for (int i = 0; i < 4; ++i) cc[0][n][i] = cc[1][n][i] = 0.f;
   };
   // -z in units: 2^23 + z by one OR, and one exact fused multiply-add
   auto minus_z = [&](int i, int j) -> float {
@@ -498,6 +496,16 @@ __device__ __forceinline__ void stage_products(
   };
   // acc += D (c - z s) for group j of the stage
   auto flush = [&](int j) {
+    float s[NT][2];  // of the lane's accumulator columns 2t, 2t + 1
+    if constexpr (!kCentre) {
+      const int from = 8 * (lane & 3) + (G16 ? j >> 1 : j0 + j);
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+        const float v = G16 && (j & 1) ? sums[n].y : sums[n].x;
+        s[n][0] = __shfl_sync(0xffffffffu, v, from);
+        s[n][1] = __shfl_sync(0xffffffffu, v, from + 4);
+      }
+    }
 #pragma unroll
     for (int rt = 0; rt < 2; ++rt) {
       const float d0 = delta_at(2 * rt, j), d1 = delta_at(2 * rt + 1, j);
@@ -526,11 +534,6 @@ __device__ __forceinline__ void stage_products(
     for (int rt = 0; rt < 2; ++rt)
       mma_f16(cc[rt][n], p[rt][0][2 * h], p[rt][1][2 * h],
               p[rt][0][2 * h + 1], p[rt][1][2 * h + 1], b0, b1);
-    if constexpr (!kCentre) {
-      const uint32_t o0 = ones<BITS, G16>(2 * h);
-      const uint32_t o1 = ones<BITS, G16>(2 * h + 1);
-      mma_f16(s[n], o0, o0, o1, o1, b0, b1);
-    }
   };
   clear();
 #pragma unroll
@@ -643,6 +646,8 @@ struct Tile {
                            // piece
   bool fresh;
   const uint4* xp[NTMAX];  // the lane's activations at the next stage
+  const float* sp[NTMAX];  // its column's group sums
+  float2 sums[NTMAX];
   int64_t term;
   float acc[2][NTMAX][4];
 
@@ -651,10 +656,13 @@ struct Tile {
       : f(lane_ & 3), ring(ring_), lane(lane_), stage(0), piece(0),
         term(term_) {}
 
-  // Starts a tile with `cols` columns; row(col) gives a column's activations
-  // (columns past the last repeat column 0: their results are dropped).
+  // Starts a tile with `cols` columns at chunk c; row(col) gives a column's
+  // row of the activations x and their group sums (columns past the last
+  // repeat column 0: their results are dropped).
   template <typename RF>
-  __device__ __forceinline__ void start(int cols, int c, RF&& row) {
+  __device__ __forceinline__ void start(const Packed& m, const uint4* x,
+                                        const float* sum, int cols, int c,
+                                        RF&& row) {
     nt = (cols + 7) / 8;
     fresh = true;
 #pragma unroll
@@ -662,7 +670,9 @@ struct Tile {
 #pragma unroll
       for (int i = 0; i < 4; ++i) acc[0][n][i] = acc[1][n][i] = 0.f;
       const int col = n * 8 + (lane >> 2);
-      xp[n] = row(col < cols ? col : 0) + c * 16 + (lane & 3);
+      const int64_t r = row(col < cols ? col : 0);
+      xp[n] = x + r * (m.blocks * 4) + c * 16 + (lane & 3);
+      sp[n] = sum + r * m.ldg;
     }
   }
   // Chunks c .. c_end - 1; next() issues the copies that refill the ring.
@@ -681,6 +691,16 @@ struct Tile {
       if (fresh || m.new_piece(c)) {
         piece = piece + 1 == S ? 0 : piece + 1;
         fresh = false;
+        if constexpr (MODE != kExact) {
+#pragma unroll
+          for (int n = 0; n < NT; ++n) {
+            if constexpr (G16)
+              sums[n] = *reinterpret_cast<const float2*>(sp[n] + c * 8 +
+                                                         2 * (lane & 3));
+            else
+              sums[n].x = sp[n][(c >> LG) * 4 + (lane & 3)];
+          }
+        }
       }
       const uint8_t* st = ring + stage * kStage<BITS>;
       const uint8_t* dd = ring + S * kStage<BITS> +
@@ -689,10 +709,10 @@ struct Tile {
       const int nb = m.blocks - 4 * c;
       if (nb >= 4)
         stage_products<BITS, G16, LG, true, MODE, NT, NTMAX>(
-            st, dd, j0, f, 4, xp, term, xv, acc, lane);
+            st, dd, j0, f, 4, xp, term, xv, sums, acc, lane);
       else
         stage_products<BITS, G16, LG, false, MODE, NT, NTMAX>(
-            st, dd, j0, f, nb, xp, term, xv, acc, lane);
+            st, dd, j0, f, nb, xp, term, xv, sums, acc, lane);
 #pragma unroll
       for (int n = 0; n < NT; ++n) xp[n] += 16;
       stage = stage + 1 == S ? 0 : stage + 1;
@@ -737,30 +757,45 @@ __global__ void __launch_bounds__(kThreads, 2)
   const int rs = a.rs, ks = kWarps / rs;
   const int wr = warp % rs, wk = warp / rs;
   const int tiles = a.I / 16, rows = (tiles + rs - 1) / rs;
-  const int units = l.entries * rows;
   const int chunks = (a.K + kChunk - 1) / kChunk;
   const int c0 = wk * chunks / ks, c1 = (wk + 1) * chunks / ks;
   const Packed m(a.codes, a.delta, a.zero, a.K, BITS, a.group);
   Stream<BITS, G16> w(m, a.I, lane);
 
+  // units: (entry, row of rs tiles), a step of gridDim.x at a time
+  struct Unit {
+    int en, row;
+  };
+  const int step_en = gridDim.x / rows, step_row = gridDim.x - step_en * rows;
+  auto next_unit = [&](Unit& u) {
+    u.en += step_en;
+    u.row += step_row;
+    if (u.row >= rows) {
+      u.row -= rows;
+      ++u.en;
+    }
+  };
+  Unit first;
+  first.en = blockIdx.x / rows;
+  first.row = blockIdx.x - first.en * rows;
   // the warp's stages: its chunks of the CTA's units, one after the other
-  int iu = blockIdx.x;
+  Unit iu = first;
   auto seek = [&]() {
     // the warp's tile of unit iu, skipping units in which it has none
-    for (; iu < units && c0 < c1; iu += gridDim.x) {
-      const int en = iu / rows, tile = (iu - en * rows) * rs + wr;
+    for (; iu.en < l.entries && c0 < c1; next_unit(iu)) {
+      const int tile = iu.row * rs + wr;
       if (tile < tiles) {
-        w.seek(m, (int64_t)l.expert[en] * 2 * a.I + tile * 16, c0);
+        w.seek(m, (int64_t)l.expert[iu.en] * 2 * a.I + tile * 16, c0);
         return;
       }
     }
-    iu = units;
+    iu.en = l.entries;
   };
   auto issue = [&]() {
-    if (iu < units) {
+    if (iu.en < l.entries) {
       w.copy(m, ring_at, lane);
       if (w.c == c1) {
-        iu += gridDim.x;
+        next_unit(iu);
         seek();
       }
     }
@@ -773,13 +808,12 @@ __global__ void __launch_bounds__(kThreads, 2)
   griddep_enter();
 
   TileT tl(ring, lane, (int64_t)a.T * a.K / 8);
-  for (int u = blockIdx.x; u < units; u += gridDim.x) {
-    const int en = u / rows, tile = (u - en * rows) * rs + wr;
+  for (Unit u = first; u.en < l.entries; next_unit(u)) {
+    const int en = u.en, tile = u.row * rs + wr;
     const int cols = l.cols[en], col0 = l.first[en];
     const bool live = tile < tiles;
-    tl.start(cols, c0, [&](int col) {
-      return a.xhat + (int64_t)(l.slot[col0 + col] / a.top_k) * (a.K / 8);
-    });
+    tl.start(m, a.xhat, a.xsum, cols, c0,
+             [&](int col) { return (int64_t)l.token[col0 + col]; });
     if (live) tl.template run<LG>(m, c0, c1, issue);
     if (ks > 1) {
       // parts of K to the warp of part 0
@@ -826,7 +860,7 @@ __global__ void __launch_bounds__(kThreads, 2)
           const int col = n * 8 + 2 * (lane & 3) + i;
           if (col < cols) {
             const int slot = l.slot[col0 + col];
-            const float un = row_unscale(a.xmax[slot / a.top_k], most);
+            const float un = row_unscale(a.xmax[l.token[col0 + col]], most);
             float* h = a.h + (int64_t)slot * a.I + ch;
             h[0] = gated(tl.acc[0][n][i] * per_unit * un, a.act) *
                    (tl.acc[1][n][i] * per_unit * un) * mid0;
@@ -904,9 +938,8 @@ __global__ void __launch_bounds__(kThreads, 2)
   int s = s0, en = s0 / chunks, c = s0 - en * chunks;
   while (s < s1) {
     const int cols = l.cols[en], col0 = l.first[en];
-    tl.start(cols, c, [&](int col) {
-      return a.hhat + (int64_t)l.slot[col0 + col] * (a.I / 8);
-    });
+    tl.start(m, a.hhat, a.hsum, cols, c,
+             [&](int col) { return (int64_t)l.slot[col0 + col]; });
     const int stop = min(s1, s + chunks - c);
     tl.template run<LG>(m, c, c + stop - s, issue);
     s = stop;
@@ -924,7 +957,7 @@ __global__ void __launch_bounds__(kThreads, 2)
           const float wt =
               l.weight[col0 + col] * row_unscale(a.hmax[slot], most) *
               per_unit;
-          float* y = mine + slot / a.top_k * kRows + g;
+          float* y = mine + l.token[col0 + col] * kRows + g;
           y[0] = fmaf(wt, tl.acc[0][n][i], y[0]);
           y[8] = fmaf(wt, tl.acc[0][n][2 + i], y[8]);
           y[16] = fmaf(wt, tl.acc[1][n][i], y[16]);
