@@ -13,6 +13,7 @@
 
 #include "common.cuh"
 #include "kernels.h"
+#include "mma16.cuh"
 
 namespace ttq {
 namespace {
@@ -115,54 +116,370 @@ __global__ void __launch_bounds__(kPlanThreads)
   }
 }
 
+// ttq_adapters_add, one launch. A cluster of CTAs takes one tile: up to 32
+// tokens of one adapter.
+//   1. U = X A^T for the tile: A's ranks as M, the tokens as N of mma.sync
+//      m16n8k16, K split over the cluster's warps, every value of X and A read
+//      once and straight into its fragment (a lane takes 8 consecutive k).
+//      Warps add through shared memory, CTAs through distributed shared
+//      memory, in order.
+//   2. out = Y + scale U B^T: tokens as M, 32 output channels as four tiles of
+//      8 whose columns are dealt so that a lane ends with 8 consecutive
+//      channels of its tokens: Y is read and written 16 bytes at a time. The
+//      cluster's warps split N; the first channels' B and Y are on their way
+//      while U is being added up.
+// U stays fp32 until it enters step 2, in two 16-bit terms (fp16 ones with a
+// power of two per token, since U may leave fp16's range) or three bf16 terms
+// for fp32. Bound by HBM: X once, Y once in and once out, A and B once per
+// adapter in use from HBM (once per tile from L2).
 constexpr int kThreads = 256;
+constexpr int kWarps = kThreads / 32;
+constexpr int kCols = 32;  // output channels of a warp's unit
 
-// One CTA per (tile, token of the tile).
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile(
+      "barrier.cluster.arrive.release.aligned;\n\t"
+      "barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+__device__ __forceinline__ float ld_cluster_f32(uint32_t a, uint32_t rank) {
+  float v;
+  asm volatile(
+      "{\n\t.reg .u32 r;\n\t"
+      "mapa.shared::cluster.u32 r, %1, %2;\n\t"
+      "ld.shared::cluster.f32 %0, [r];\n\t}"
+      : "=f"(v)
+      : "r"(a), "r"(rank)
+      : "memory");
+  return v;
+}
+
 template <typename TX, typename TY>
-__global__ void __launch_bounds__(kThreads)
-    adapters_add_kernel(const TX* __restrict__ X, int T, int K, int64_t ldx,
-                        const TX* __restrict__ A, const TX* __restrict__ B,
-                        const float* __restrict__ scale, int L, int r, int N,
-                        const int32_t* __restrict__ plan, int tiles_max,
-                        const TY* Y, int64_t ldy, TY* out, int64_t ldo,
-                        uint32_t* err) {
-  __shared__ float U[64];
-  griddep_enter();
-  if (plan[1] != kTile || plan[2] != T || plan[3] != L) {
-    if (threadIdx.x == 0) flag_error(err, TTQ_DEVERR_INDEX);
-    return;
-  }
-  if ((int)blockIdx.x >= plan[0]) return;
-  const int4 tl = reinterpret_cast<const int4*>(plan + kHead)[blockIdx.x];
-  if ((int)blockIdx.y >= tl.z) return;
-  const int64_t t =
-      plan[kHead + 4 * (int64_t)tiles_max + tl.y + blockIdx.y];
-  const TY* y = Y + t * ldy;
-  TY* o = out + t * ldo;
-  if (tl.x < 0) {
-    if (y != o)
-      for (int n = threadIdx.x; n < N; n += kThreads) o[n] = y[n];
-    return;
-  }
-  const TX* a = A + (int64_t)tl.x * r * K;
-  const TX* b = B + (int64_t)tl.x * N * r;
-  for (int q = threadIdx.x >> 5; q < r; q += kThreads / 32) {
-    float acc = 0.f;
-    for (int j = threadIdx.x & 31; j < K; j += 32)
-      acc = fmaf(to_f32(X[t * ldx + j]), to_f32(a[(int64_t)q * K + j]), acc);
+struct AddArgs {
+  const TX *X, *A, *B;
+  const float* scale;
+  const int32_t* plan;
+  const TY* Y;
+  TY* out;
+  int64_t ldx, ldy, ldo;
+  int T, K, L, r, N, tiles_max;
+  bool vec;  // rows of Y and out on 16-byte boundaries
+  uint32_t* err;
+};
+
+// The terms U enters the second product in.
+template <typename TX>
+constexpr int kUTerms = sizeof(TX) == 4 ? 3 : 2;
+
+template <typename TX, int MT>
+constexpr int kFrags = MT * 2 * kUTerms<TX>;  // of U: k16 x m-tile x term
+
+template <typename TX, int MT>
+constexpr size_t smem_bytes() {
+  // warps' sums (reused for U's fragments), the CTA's U, its sum
+  const size_t red = (size_t)kWarps * MT * 4 * 128 * 4;
+  const size_t frag = (size_t)kFrags<TX, MT> * 32 * 16;
+  return (red > frag ? red : frag) + (size_t)MT * 16 * kTile * 4 * 2 +
+         kTile * 4;
+}
+
+// NT: tiles of 8 tokens (1 or 4).
+template <typename TX, typename TY, int MT, int NT>
+__device__ __forceinline__ void add_tile(const AddArgs<TX, TY>& a, int4 tl,
+                                         const int32_t* order, int rank,
+                                         int ranks, float* sm) {
+  using namespace mma16;
+  constexpr int TM = NT == 1 ? 1 : 2;  // tiles of 16 tokens in step 2
+  constexpr int XT = mma16::kTerms<TX, TX>, UT = kUTerms<TX>;
+  constexpr bool HALF = kHalf<TX, TX>;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int g = lane >> 2, t = lane & 3;
+  const int parts = ranks * kWarps, part = rank * kWarps + warp;
+  float* red = sm;                                   // [warp][m][n][128]
+  uint4* frag = reinterpret_cast<uint4*>(sm);        // [kk][m][term][lane]
+  float* upart = sm + (smem_bytes<TX, MT>() / 4 - MT * 16 * kTile * 2 - kTile);
+  float* U = upart + MT * 16 * kTile;                // [token][rank]
+  float* down = U + MT * 16 * kTile;                 // per token: 2^-e scale
+
+  // ---- step 1
+  const TX* xr[NT];
 #pragma unroll
-    for (int s = 16; s > 0; s >>= 1)
-      acc += __shfl_xor_sync(0xffffffffu, acc, s);
-    if ((threadIdx.x & 31) == 0) U[q] = acc;
+  for (int n = 0; n < NT; ++n) {
+    const int i = n * 8 + g;
+    xr[n] = a.X + (int64_t)order[i < tl.z ? i : 0] * a.ldx;
+  }
+  const TX* A = a.A + (int64_t)tl.x * a.r * a.K;
+  float acc[MT][NT][4] = {};
+  const int blocks = (a.K + 31) / 32;
+  const int b0 = (int)((int64_t)blocks * part / parts);
+  const int b1 = (int)((int64_t)blocks * (part + 1) / parts);
+  constexpr int UN = MT * 2 + NT <= 6 && XT == 1 ? 4 : 2;  // blocks in flight
+  for (int bb = b0; bb < b1; bb += UN) {
+    Raw<TX, 8> ra[UN][MT][2], rx[UN][NT];
+#pragma unroll
+    for (int u = 0; u < UN; ++u) {
+      const int k = (bb + u) * 32 + 8 * t;
+      const bool ok = bb + u < b1 && k < a.K;
+#pragma unroll
+      for (int m = 0; m < MT; ++m)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const int q = m * 16 + h * 8 + g;
+          load<TX, 8>(A + (int64_t)q * a.K + k, ok && q < a.r, ra[u][m][h]);
+        }
+#pragma unroll
+      for (int n = 0; n < NT; ++n) load<TX, 8>(xr[n] + k, ok, rx[u][n]);
+    }
+#pragma unroll
+    for (int u = 0; u < UN; ++u) {
+      uint32_t xt[NT][XT][4];
+#pragma unroll
+      for (int n = 0; n < NT; ++n) terms<TX, TX, 8>(rx[u][n], xt[n]);
+#pragma unroll
+      for (int m = 0; m < MT; ++m) {
+        uint32_t at[2][XT][4];
+        terms<TX, TX, 8>(ra[u][m][0], at[0]);
+        terms<TX, TX, 8>(ra[u][m][1], at[1]);
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+          for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int i = 0; i < XT; ++i)
+#pragma unroll
+              for (int j = 0; j + i < XT; ++j)
+                mma<HALF>(acc[m][n], at[0][i][2 * h], at[1][i][2 * h],
+                          at[0][i][2 * h + 1], at[1][i][2 * h + 1],
+                          xt[n][j][2 * h], xt[n][j][2 * h + 1]);
+      }
+    }
+  }
+#pragma unroll
+  for (int m = 0; m < MT; ++m)
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+      *reinterpret_cast<float4*>(red + ((warp * MT + m) * NT + n) * 128 +
+                                 lane * 4) =
+          make_float4(acc[m][n][0], acc[m][n][1], acc[m][n][2], acc[m][n][3]);
+
+  // ---- the first unit of step 2: B and Y need not wait for U
+  const TX* B = a.B + (int64_t)tl.x * a.N * a.r;
+  int64_t yt[TM][2], ot[TM][2];  // rows of the lane's tokens
+  bool live[TM][2];
+#pragma unroll
+  for (int m = 0; m < TM; ++m)
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int i = m * 16 + h * 8 + g;
+      live[m][h] = i < tl.z;
+      const int64_t tok = order[live[m][h] ? i : 0];
+      yt[m][h] = tok * a.ldy;
+      ot[m][h] = tok * a.ldo;
+    }
+  const int units = (a.N + kCols - 1) / kCols;
+  struct Unit {
+    Raw<TX, 4> b[4][MT];
+    Raw<TY, 8> y[TM][2];
+  };
+  auto fetch = [&](int u, Unit& f) {
+    const int n0 = u * kCols;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int n = n0 + 8 * (g >> 1) + 2 * j + (g & 1);
+#pragma unroll
+      for (int kk = 0; kk < MT; ++kk) {
+        const int q = kk * 16 + 4 * t;
+        load<TX, 4>(B + (int64_t)n * a.r + q, n < a.N && q < a.r, f.b[j][kk]);
+      }
+    }
+    const int n = n0 + 8 * t;
+#pragma unroll
+    for (int m = 0; m < TM; ++m)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const TY* y = a.Y + yt[m][h] + n;
+        if (a.vec && n + 8 <= a.N) {
+          load<TY, 8>(y, live[m][h], f.y[m][h]);
+        } else {
+          TY e[8];
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            e[i] = live[m][h] && n + i < a.N ? y[i] : from_f32<TY>(0.f);
+          f.y[m][h] = *reinterpret_cast<const Raw<TY, 8>*>(e);
+        }
+      }
+  };
+  Unit cur;
+  if (part < units) fetch(part, cur);
+
+  // ---- U: the warps', then the cluster's sums
+  __syncthreads();
+  constexpr int kElems = MT * NT * 128;
+  for (int i = tid; i < kElems; i += kThreads) {
+    float v = 0.f;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) v += red[w * kElems + i];
+    upart[i] = v;
+  }
+  if (ranks > 1)
+    cluster_sync();
+  else
+    __syncthreads();
+  const float sc = a.scale ? a.scale[tl.x] : 1.f;
+  const uint32_t up = smem_u32(upart);
+  for (int i = tid; i < kElems; i += kThreads) {
+    float v = 0.f;
+    if (ranks > 1) {
+      for (int q = 0; q < ranks; ++q) v += ld_cluster_f32(up + i * 4, q);
+    } else {
+      v = upart[i];
+    }
+    // element: tile (m, n), lane, register -> rank, token
+    const int e = i & 127, mn = i >> 7, ln = e >> 2, rg = e & 3;
+    const int q = mn / NT * 16 + (ln >> 2) + 8 * (rg >> 1);
+    const int tok = mn % NT * 8 + 2 * (ln & 3) + (rg & 1);
+    U[tok * (MT * 16) + q] = v * sc;
+  }
+  if (ranks > 1)
+    cluster_sync();  // every CTA has read upart: nothing leaves before that
+  else
+    __syncthreads();
+  // U's fragments: token rows g and g + 8, ranks 4t .. 4t + 3 of each 16
+  if constexpr (HALF) {
+    // a power of two per token brings its largest U to [2^13, 2^14)
+    for (int i = tid; i < 16 * TM; i += kThreads) {
+      uint32_t mx = 0;
+      if (i < NT * 8)
+        for (int q = 0; q < MT * 16; ++q)
+          mx = max(mx, __float_as_uint(U[i * (MT * 16) + q]) & 0x7FFFFFFFu);
+      const int k = min(13 - ((int)(mx >> 23) - 127), 126);
+      down[i] = __uint_as_float((uint32_t)(127 - k) << 23);
+    }
+    __syncthreads();
+  }
+  for (int i = tid; i < MT * TM * 32; i += kThreads) {
+    const int ln = i & 31, m = (i >> 5) % TM, kk = (i >> 5) / TM;
+    const int row = m * 16 + (ln >> 2), q = kk * 16 + 4 * (ln & 3);
+    float v[8];  // (row, q), (row, q + 1), (row + 8, ..), (row, q + 2), ..
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const int rr = row + ((e >> 1) & 1) * 8, qq = q + (e >> 2) * 2 + (e & 1);
+      v[e] = rr < NT * 8 ? U[rr * (MT * 16) + qq] : 0.f;
+      if constexpr (HALF)  // exact; a row without values has down = 2^-126
+        v[e] = rr < NT * 8 ? v[e] / down[rr] : 0.f;
+    }
+    uint4* o = frag + (kk * TM + m) * UT * 32 + ln;
+    if constexpr (HALF) {
+      uint32_t w[4];
+#pragma unroll
+      for (int k = 0; k < UT; ++k) {
+#pragma unroll
+        for (int p = 0; p < 4; ++p) {
+          w[p] = f16x2(v[2 * p], v[2 * p + 1]);
+          float x, y;
+          f16x2_to_f32(w[p], x, y);
+          v[2 * p] -= x;
+          v[2 * p + 1] -= y;
+        }
+        o[k * 32] = make_uint4(w[0], w[1], w[2], w[3]);
+      }
+    } else {
+      uint32_t w[UT][4];
+      split<UT, 4>(v, w);
+#pragma unroll
+      for (int k = 0; k < UT; ++k)
+        o[k * 32] = make_uint4(w[k][0], w[k][1], w[k][2], w[k][3]);
+    }
   }
   __syncthreads();
-  const float sc = scale ? scale[tl.x] : 1.f;
-  for (int n = threadIdx.x; n < N; n += kThreads) {
-    float acc = 0.f;
-    for (int q = 0; q < r; ++q)
-      acc = fmaf(U[q], to_f32(b[(int64_t)n * r + q]), acc);
-    o[n] = from_f32<TY>(fmaf(sc, acc, to_f32(y[n])));
+
+  // ---- step 2
+  for (int u = part; u < units; u += parts) {
+    float c[TM][4][4] = {};
+#pragma unroll
+    for (int kk = 0; kk < MT; ++kk) {
+      uint32_t bt[4][XT][2];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) terms<TX, TX, 4>(cur.b[j][kk], bt[j]);
+#pragma unroll
+      for (int m = 0; m < TM; ++m)
+#pragma unroll
+        for (int k = 0; k < UT; ++k) {
+          const uint4 f = frag[((kk * TM + m) * UT + k) * 32 + lane];
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+#pragma unroll
+            for (int x = 0; x < XT; ++x)
+              if (k + x < UT)
+                mma<HALF>(c[m][j], f.x, f.y, f.z, f.w, bt[j][x][0],
+                          bt[j][x][1]);
+        }
+    }
+    const Unit now = cur;
+    if (u + parts < units) fetch(u + parts, cur);
+    const int n = u * kCols + 8 * t;
+#pragma unroll
+    for (int m = 0; m < TM; ++m)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        if (!live[m][h]) continue;
+        const float s = HALF ? down[m * 16 + h * 8 + g] : 1.f;
+        TY e[8];
+        *reinterpret_cast<Raw<TY, 8>*>(e) = now.y[m][h];
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          e[i] = from_f32<TY>(
+              fmaf(c[m][i >> 1][2 * h + (i & 1)], s, to_f32(e[i])));
+        TY* o = a.out + ot[m][h] + n;
+        if (a.vec && n + 8 <= a.N) {
+          const Raw<TY, 8>& w = *reinterpret_cast<const Raw<TY, 8>*>(e);
+#pragma unroll
+          for (int i = 0; i < (int)sizeof(TY) / 2; ++i)
+            reinterpret_cast<uint4*>(o)[i] =
+                make_uint4(w.w[4 * i], w.w[4 * i + 1], w.w[4 * i + 2],
+                           w.w[4 * i + 3]);
+        } else {
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            if (n + i < a.N) o[i] = e[i];
+        }
+      }
   }
+}
+
+template <typename TX, typename TY, int MT>
+__global__ void __launch_bounds__(kThreads)
+    adapters_add_kernel(const AddArgs<TX, TY> a) {
+  extern __shared__ __align__(16) float sm[];
+  griddep_enter();
+  // every exit below is the whole cluster's: it has one tile
+  if (a.plan[1] != kTile || a.plan[2] != a.T || a.plan[3] != a.L) {
+    if (threadIdx.x == 0) flag_error(a.err, TTQ_DEVERR_INDEX);
+    return;
+  }
+  if ((int)blockIdx.x >= a.plan[0]) return;
+  const int4 tl = reinterpret_cast<const int4*>(a.plan + kHead)[blockIdx.x];
+  const int32_t* order = a.plan + kHead + 4 * (int64_t)a.tiles_max + tl.y;
+  const int rank = blockIdx.y, ranks = gridDim.y;
+  if (tl.x < 0) {
+    if (a.Y == a.out) return;
+    for (int i = 0; i < tl.z; ++i) {
+      const TY* y = a.Y + (int64_t)order[i] * a.ldy;
+      TY* o = a.out + (int64_t)order[i] * a.ldo;
+      constexpr int E = 16 / sizeof(TY);
+      const int whole = a.vec ? a.N / E : 0;
+      for (int n = rank * kThreads + threadIdx.x; n < whole;
+           n += ranks * kThreads)
+        reinterpret_cast<uint4*>(o)[n] = reinterpret_cast<const uint4*>(y)[n];
+      for (int n = whole * E + rank * kThreads + threadIdx.x; n < a.N;
+           n += ranks * kThreads)
+        o[n] = y[n];
+    }
+    return;
+  }
+  if (tl.z <= 8)
+    add_tile<TX, TY, MT, 1>(a, tl, order, rank, ranks, sm);
+  else
+    add_tile<TX, TY, MT, 4>(a, tl, order, rank, ranks, sm);
 }
 
 }  // namespace
@@ -183,17 +500,51 @@ ttq_status launch_adapters_plan(const int32_t* index, int64_t T, int64_t L,
 
 ttq_status launch_adapters_add(const AdapterArgs& a, cudaStream_t st) {
   LaunchShape ls;
-  ls.grid = dim3((unsigned)max_tiles(a.T, a.L), kTile);
+  const int tiles = (int)max_tiles(a.T, a.L);
+  // up to 8 CTAs share a tile: as many as fill two per SM
+  const int ranks = std::max(1, std::min(8, 2 * sm_count() / tiles));
+  ls.grid = dim3((unsigned)tiles, (unsigned)ranks);
   ls.block = dim3(kThreads);
-  auto go = [&](auto* x, auto* y) {
+  ls.cluster_y = (unsigned)ranks;
+  auto go = [&](auto* x, auto* y) -> ttq_status {
     using TX = std::remove_const_t<std::remove_pointer_t<decltype(x)>>;
     using TY = std::remove_pointer_t<decltype(y)>;
-    return launch(ls, st, adapters_add_kernel<TX, TY>, x, (int)a.T, (int)a.K,
-                  a.ldx, static_cast<const TX*>(a.A),
-                  static_cast<const TX*>(a.B), a.scale, (int)a.L, a.r,
-                  (int)a.N, a.plan, (int)max_tiles(a.T, a.L),
-                  static_cast<const TY*>(a.Y), a.ldy, y, a.ldo,
-                  device_error_word());
+    AddArgs<TX, TY> g;
+    g.X = x;
+    g.A = static_cast<const TX*>(a.A);
+    g.B = static_cast<const TX*>(a.B);
+    g.scale = a.scale;
+    g.plan = a.plan;
+    g.Y = static_cast<const TY*>(a.Y);
+    g.out = y;
+    g.ldx = a.ldx;
+    g.ldy = a.ldy;
+    g.ldo = a.ldo;
+    g.T = (int)a.T;
+    g.K = (int)a.K;
+    g.L = (int)a.L;
+    g.r = a.r;
+    g.N = (int)a.N;
+    g.tiles_max = tiles;
+    const uintptr_t at = reinterpret_cast<uintptr_t>(a.Y) |
+                         reinterpret_cast<uintptr_t>(a.out) |
+                         (uintptr_t)(a.ldy * sizeof(TY)) |
+                         (uintptr_t)(a.ldo * sizeof(TY));
+    g.vec = at % 16 == 0;
+    g.err = device_error_word();
+    auto run = [&](auto mt) -> ttq_status {
+      constexpr int MT = decltype(mt)::value;
+      ls.smem = smem_bytes<TX, MT>();
+      auto kern = adapters_add_kernel<TX, TY, MT>;
+      if (cudaFuncSetAttribute(kern,
+                               cudaFuncAttributeMaxDynamicSharedMemorySize,
+                               (int)ls.smem) != cudaSuccess)
+        return TTQ_ERR_CUDA;
+      return launch(ls, st, kern, g);
+    };
+    if (a.r <= 16) return run(std::integral_constant<int, 1>{});
+    if (a.r <= 32) return run(std::integral_constant<int, 2>{});
+    return run(std::integral_constant<int, 4>{});
   };
   auto go_y = [&](auto* x) {
     if (a.yt == TTQ_F32) return go(x, static_cast<float*>(a.out));
