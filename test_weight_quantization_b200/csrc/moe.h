@@ -50,6 +50,25 @@ __host__ __device__ inline int row_exponent(uint32_t max_bits, int most) {
   return k < 126 ? k : 126;
 }
 
+// Bytes of `rows` rows of `width` channels in fp16 terms with their sums, and
+// whether the expert kernels hold them in shared memory: what is left beside
+// the largest rings when two CTAs share an SM.
+inline size_t rows_bytes(int64_t rows, int64_t width, int group, int terms) {
+  const int64_t sums = (width / group + 15) / 16 * 16;  // groups_ld
+  return (size_t)(rows * width * 2 * terms + rows * sums * 4 + 16);
+}
+inline bool rows_fit(int64_t rows, int64_t width, int group, int terms) {
+  return rows <= 8 && rows_bytes(rows, width, group, terms) <= 18 * 1024;
+}
+
+// What every row of activations is converted by (moe_rows.cuh).
+struct RowFormat {
+  int terms;  // fp16 terms
+  int group;  // channels per sum
+  int most;   // Positions::kMost
+  int4 up;    // kMost - at(i) of code pair i
+};
+
 // xhat: fp16 terms of the rows, [term][T][K], in the order the code pairs
 // want; xsum [T][groups_ld]: the rows' sums over every group (times 2^k);
 // xmax: bits of a token's largest |x|. h [T top_k][I] fp32, and
@@ -67,6 +86,13 @@ struct UpArgs {
   float* h;
   ttq_dtype yt;
   uint32_t* err;
+  // local: the rows are converted from X by every CTA
+  bool local;
+  const void* X;
+  ttq_dtype xt;
+  int64_t ldx;
+  const float* inv_s;
+  RowFormat format;
 };
 struct DownArgs {
   const uint4* hhat;
@@ -81,6 +107,9 @@ struct DownArgs {
   void* Y;
   ttq_dtype yt;
   int64_t ldy;
+  bool local;  // the rows are converted from h by every CTA
+  const float* h;
+  RowFormat format;
 };
 
 template <int BITS, typename Args>

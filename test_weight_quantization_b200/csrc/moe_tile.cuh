@@ -35,6 +35,7 @@
 #include "common.cuh"
 #include "kernels.h"
 #include "moe.h"
+#include "moe_rows.cuh"
 
 namespace ttq {
 namespace moe {
@@ -61,6 +62,12 @@ template <int BITS>
 constexpr int kStages = BITS <= 3 ? 5 : BITS <= 5 ? 3 : 2;
 template <int BITS, bool G16>
 constexpr int kRing = kStages<BITS> * (kStage<BITS> + kPiece<G16>);
+// Where the rows a CTA converts itself start: after the rings, which start at
+// byte `ring`.
+template <int BITS, bool G16>
+constexpr int smem_rows(int ring) {
+  return ring + 8 * kRing<BITS, G16>;
+}
 
 // ------------------------------------------------------------- columns ---
 
@@ -108,6 +115,60 @@ __device__ __forceinline__ void build_lists(Lists& l, const int32_t* ids,
                                             int top_k, int E, uint32_t* err) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int n = T * top_k;
+  if (n <= 32) {
+    // one choice per lane: every warp finds the groups by matching, the first
+    // writes them
+    const int e = lane < n ? ids[lane] : -1, t = lane / top_k;
+    float w = weights && lane < n ? weights[lane] : 0.f;
+    if (e >= E && err && blockIdx.x == 0) flag_error(err, TTQ_DEVERR_INDEX);
+    const bool valid = e >= 0 && e < E;
+    const unsigned same = __match_any_sync(0xffffffffu, valid ? e : -1);
+    const unsigned below = (1u << lane) - 1u;
+    const unsigned token =
+        (top_k == 32 ? 0xffffffffu : (1u << top_k) - 1u) << (t * top_k);
+    // the first of a token's equal choices stands for all of them
+    const unsigned mine = same & token;
+    const bool first = valid && (mine & below) == 0;
+    const float w0 = w;
+    if (__any_sync(0xffffffffu, valid && mine != (1u << lane))) {
+      w = 0.f;
+      for (int q = 0; q < 32; ++q) {
+        const float v = __shfl_sync(0xffffffffu, w0, q);
+        if (mine >> q & 1) w += v;
+      }
+    }
+    const unsigned firsts = __ballot_sync(0xffffffffu, first);
+    const unsigned cols = same & firsts;  // the expert's columns
+    const bool leads = first && (cols & below) == 0;
+    const unsigned leaders = __ballot_sync(0xffffffffu, leads);
+    // columns of the experts led by lower lanes
+    int at = leads ? __popc(cols) : 0;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int v = __shfl_up_sync(0xffffffffu, at, o);
+      if (lane >= o) at += v;
+    }
+    const int start = at - __popc(cols);  // of the leader's own
+    const int lead = cols ? __ffs(cols) - 1 : 0;
+    const int from = __shfl_sync(0xffffffffu, start, lead);
+    l.entries = __popc(leaders);
+    if (warp == 0) {
+      if (first) {
+        const int c = from + __popc(cols & below);
+        l.slot[c] = (uint16_t)lane;
+        l.token[c] = (uint8_t)t;
+        l.weight[c] = w;
+      }
+      if (leads) {
+        const int i = __popc(leaders & below);
+        l.expert[i] = (int16_t)e;
+        l.first[i] = (int16_t)start;
+        l.cols[i] = (int16_t)__popc(cols);
+      }
+    }
+    __syncthreads();
+    return;
+  }
   for (int e = tid; e < E; e += kThreads) l.tokens[e] = make_uint2(0, 0);
   __syncthreads();
   for (int p = tid; p < n; p += kThreads) {
@@ -736,7 +797,7 @@ struct Tile {
 // of K; units (entry, rs tiles) are taken round robin by a persistent grid.
 // Neighbouring tiles share their activations through L1; parts of K are added
 // through shared memory.
-template <int BITS, bool G16, int LG, int MODE, int NTMAX>
+template <int BITS, bool G16, int LG, int MODE, int NTMAX, bool LOCAL>
 __global__ void __launch_bounds__(kThreads, 2)
     up_kernel(const UpArgs a) {
   using TileT = Tile<BITS, G16, MODE, NTMAX>;
@@ -807,12 +868,36 @@ __global__ void __launch_bounds__(kThreads, 2)
   for (int i = 0; i < S - 1; ++i) issue();
   griddep_enter();
 
+  const uint4* xhat = a.xhat;
+  const float* xsum = a.xsum;
+  const uint32_t* xmax = a.xmax;
+  if constexpr (LOCAL) {
+    uint4* x = reinterpret_cast<uint4*>(sm + smem_rows<BITS, G16>(
+        (int)(reinterpret_cast<const uint8_t*>(red) - sm) +
+        kWarps * 2 * NTMAX * 128 * 4));
+    float* sum = reinterpret_cast<float*>(
+        x + (int64_t)a.T * a.K / 8 * a.format.terms);
+    uint32_t* mx = reinterpret_cast<uint32_t*>(sum + a.T * m.ldg);
+    auto convert = [&](auto* rows) {
+      convert_rows<kThreads>(a.format, a.T, a.K / 8, a.inv_s, x, sum, m.ldg,
+                             mx, [&](int r) { return rows + r * a.ldx; });
+    };
+    if (a.xt == TTQ_F32)
+      convert(static_cast<const float*>(a.X));
+    else if (a.xt == TTQ_BF16)
+      convert(static_cast<const __nv_bfloat16*>(a.X));
+    else
+      convert(static_cast<const __half*>(a.X));
+    xhat = x;
+    xsum = sum;
+    xmax = mx;
+  }
   TileT tl(ring, lane, (int64_t)a.T * a.K / 8);
   for (Unit u = first; u.en < l.entries; next_unit(u)) {
     const int en = u.en, tile = u.row * rs + wr;
     const int cols = l.cols[en], col0 = l.first[en];
     const bool live = tile < tiles;
-    tl.start(m, a.xhat, a.xsum, cols, c0,
+    tl.start(m, xhat, xsum, cols, c0,
              [&](int col) { return (int64_t)l.token[col0 + col]; });
     if (live) tl.template run<LG>(m, c0, c1, issue);
     if (ks > 1) {
@@ -860,7 +945,7 @@ __global__ void __launch_bounds__(kThreads, 2)
           const int col = n * 8 + 2 * (lane & 3) + i;
           if (col < cols) {
             const int slot = l.slot[col0 + col];
-            const float un = row_unscale(a.xmax[l.token[col0 + col]], most);
+            const float un = row_unscale(xmax[l.token[col0 + col]], most);
             float* h = a.h + (int64_t)slot * a.I + ch;
             h[0] = gated(tl.acc[0][n][i] * per_unit * un, a.act) *
                    (tl.acc[1][n][i] * per_unit * un) * mid0;
@@ -881,7 +966,7 @@ __global__ void __launch_bounds__(kThreads, 2)
 // are one list, split evenly over the parts of all CTAs of a cluster. Every
 // warp keeps the sums of all tokens for its share and adds an entry's columns
 // to them when it leaves the entry; parts are added at the end, in order.
-template <int BITS, bool G16, int LG, int MODE, int NTMAX>
+template <int BITS, bool G16, int LG, int MODE, int NTMAX, bool LOCAL>
 __global__ void __launch_bounds__(kThreads, 2)
     down_kernel(const DownArgs a) {
   using TileT = Tile<BITS, G16, MODE, NTMAX>;
@@ -933,12 +1018,30 @@ __global__ void __launch_bounds__(kThreads, 2)
   for (int i = 0; i < S - 1; ++i) issue();
   griddep_enter();
 
+  const uint4* hhat = a.hhat;
+  const float* hsum = a.hsum;
+  const uint32_t* hmax = a.hmax;
+  const int slots = a.T * a.top_k;
+  if constexpr (LOCAL) {
+    uint4* x = reinterpret_cast<uint4*>(sm + smem_rows<BITS, G16>(
+        (int)(reinterpret_cast<const uint8_t*>(ysum) - sm) +
+        kWarps * region * 4));
+    float* sum =
+        reinterpret_cast<float*>(x + (int64_t)slots * a.I / 8 * a.format.terms);
+    uint32_t* mx = reinterpret_cast<uint32_t*>(sum + slots * m.ldg);
+    // (the row of a choice without an expert is whatever h holds: not used)
+    convert_rows<kThreads>(a.format, slots, a.I / 8, nullptr, x, sum, m.ldg,
+                           mx, [&](int r) { return a.h + (int64_t)r * a.I; });
+    hhat = x;
+    hsum = sum;
+    hmax = mx;
+  }
   const int t = lane & 3, g = lane >> 2;
-  TileT tl(ring, lane, (int64_t)a.T * a.top_k * a.I / 8);
+  TileT tl(ring, lane, (int64_t)slots * a.I / 8);
   int s = s0, en = s0 / chunks, c = s0 - en * chunks;
   while (s < s1) {
     const int cols = l.cols[en], col0 = l.first[en];
-    tl.start(m, a.hhat, a.hsum, cols, c,
+    tl.start(m, hhat, hsum, cols, c,
              [&](int col) { return (int64_t)l.slot[col0 + col]; });
     const int stop = min(s1, s + chunks - c);
     tl.template run<LG>(m, c, c + stop - s, issue);
@@ -955,7 +1058,7 @@ __global__ void __launch_bounds__(kThreads, 2)
         if (col < cols) {
           const int slot = l.slot[col0 + col];
           const float wt =
-              l.weight[col0 + col] * row_unscale(a.hmax[slot], most) *
+              l.weight[col0 + col] * row_unscale(hmax[slot], most) *
               per_unit;
           float* y = mine + l.token[col0 + col] * kRows + g;
           y[0] = fmaf(wt, tl.acc[0][n][i], y[0]);
@@ -1043,26 +1146,29 @@ inline int pick_rs(int64_t tiles, int64_t slots) {
 
 inline int ctas_per_sm(size_t smem) { return smem + 1024 <= 114 * 1024 ? 2 : 1; }
 
-template <int BITS, bool G16, int LG, int MODE, int NTMAX>
+template <int BITS, bool G16, int LG, int MODE, int NTMAX, bool LOCAL>
 ttq_status launch_up(UpArgs u, cudaStream_t st) {
   LaunchShape ls;
   ls.block = dim3(kThreads);
   ls.smem = up_smem<BITS, G16>(NTMAX, u.T * u.top_k, u.E);
+  if (LOCAL) ls.smem += rows_bytes(u.T, u.K, u.group, u.format.terms) + 32;
   const int64_t slots = ctas_per_sm(ls.smem) * sm_count();
   const int64_t tiles =
       (int64_t)Lists::max_entries(u.T * u.top_k, u.E) * (u.I / 16);
   u.rs = pick_rs(tiles, slots);
   ls.grid = dim3((unsigned)std::min<int64_t>(tiles, slots));
-  auto kern = up_kernel<BITS, G16, LG, MODE, NTMAX>;
+  auto kern = up_kernel<BITS, G16, LG, MODE, NTMAX, LOCAL>;
   if (!allow_smem(kern, ls.smem)) return TTQ_ERR_CUDA;
   return launch(ls, st, kern, u);
 }
 
-template <int BITS, bool G16, int LG, int MODE, int NTMAX>
+template <int BITS, bool G16, int LG, int MODE, int NTMAX, bool LOCAL>
 ttq_status launch_down(DownArgs d, cudaStream_t st) {
   LaunchShape ls;
   ls.block = dim3(kThreads);
   ls.smem = down_smem<BITS, G16>(d.T, d.T * d.top_k, d.E);
+  if (LOCAL)
+    ls.smem += rows_bytes(d.T * d.top_k, d.I, d.group, d.format.terms) + 32;
   const int slots = ctas_per_sm(ls.smem) * sm_count();
   const int tiles = d.K / kRows;
   // as many neighbouring tiles as still leave a cluster of up to 8 per SM slot
@@ -1072,7 +1178,7 @@ ttq_status launch_down(DownArgs d, cudaStream_t st) {
   const int ranks = std::max(1, std::min(8, slots / grid));
   ls.grid = dim3((unsigned)grid, (unsigned)ranks);
   ls.cluster_y = (unsigned)ranks;
-  auto kern = down_kernel<BITS, G16, LG, MODE, NTMAX>;
+  auto kern = down_kernel<BITS, G16, LG, MODE, NTMAX, LOCAL>;
   if (!allow_smem(kern, ls.smem)) return TTQ_ERR_CUDA;
   return launch(ls, st, kern, d);
 }
@@ -1082,13 +1188,15 @@ ttq_status launch_down(DownArgs d, cudaStream_t st) {
 // with more than 16 tokens becomes two entries, the second read from L2.)
 template <int BITS, bool G16, int LG, int MODE>
 ttq_status launch_mode(const UpArgs& u, cudaStream_t st) {
-  return u.T <= 8 ? launch_up<BITS, G16, LG, MODE, 1>(u, st)
-                  : launch_up<BITS, G16, LG, MODE, 2>(u, st);
+  if (u.T > 8) return launch_up<BITS, G16, LG, MODE, 2, false>(u, st);
+  return u.local ? launch_up<BITS, G16, LG, MODE, 1, true>(u, st)
+                 : launch_up<BITS, G16, LG, MODE, 1, false>(u, st);
 }
 template <int BITS, bool G16, int LG, int MODE>
 ttq_status launch_mode(const DownArgs& d, cudaStream_t st) {
-  return d.T <= 8 ? launch_down<BITS, G16, LG, MODE, 1>(d, st)
-                  : launch_down<BITS, G16, LG, MODE, 2>(d, st);
+  if (d.T > 8) return launch_down<BITS, G16, LG, MODE, 2, false>(d, st);
+  return d.local ? launch_down<BITS, G16, LG, MODE, 1, true>(d, st)
+                 : launch_down<BITS, G16, LG, MODE, 1, false>(d, st);
 }
 
 template <int BITS, bool G16, int LG, typename Args>

@@ -138,16 +138,25 @@ def _check(status: int, what: str) -> None:
         raise TTQError(f"{what}: {_lib.ttq_status_string(status).decode()}")
 
 
+# The current stream's handle and the current device without building the
+# objects of torch.cuda (0.1 us instead of 3.4 us per call).
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_raw_device = getattr(torch._C, "_cuda_getDevice", None)
+
+
 def _stream() -> int:
-    return torch.cuda.current_stream().cuda_stream
+    if _raw_stream is None or _raw_device is None:
+        return torch.cuda.current_stream().cuda_stream
+    return _raw_stream(_raw_device())
 
 
 def _dev(t: torch.Tensor, name: str) -> None:
     """A CUDA tensor on the current device (the one the call launches on)."""
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise TTQError(f"{name} must be a CUDA tensor")
-    cur = torch.cuda.current_device()
-    if t.device.index != cur:
+    cur = torch.cuda.current_device() if _raw_device is None \
+        else _raw_device()
+    if t.get_device() != cur:
         raise TTQError(f"{name} is on {t.device}; the call launches on "
                        f"cuda:{cur}")
 
@@ -176,6 +185,12 @@ def _buf(t: torch.Tensor, name: str, dtypes, rows: int,
     """A dense device buffer: at least ``rows`` entries ([rows] vector), or
     at least ``rows`` rows of exactly ``cols`` entries."""
     _dev(t, name)
+    if t.dtype is dtypes:  # the usual case, first
+        shape = t.shape
+        if ((len(shape) == 1 and shape[0] >= rows) if cols is None else
+                (len(shape) == 2 and shape[0] >= rows and shape[1] == cols)) \
+                and t.is_contiguous():
+            return
     dtypes = dtypes if isinstance(dtypes, tuple) else (dtypes,)
     if t.dtype not in dtypes:
         raise TTQError(f"{name} must be {' or '.join(map(str, dtypes))}, "
