@@ -160,7 +160,6 @@ ttq_status launch_moe_lowbit(const MoeArgs& a, cudaStream_t st) {
   u.top_k = a.top_k;
   u.group = a.group;
   u.act = (int)a.act;
-  u.rs = 1;
   u.codes = a.up_codes;
   u.delta = a.up_delta;
   u.zero = a.up_zero;

@@ -78,7 +78,7 @@ struct UpArgs {
   const float* xsum;
   const uint32_t* xmax;
   const int32_t* ids;
-  int T, K, I, E, top_k, group, act, rs;
+  int T, K, I, E, top_k, group, act;
   const uint32_t* codes;
   const float* delta;
   const uint8_t* zero;

@@ -12,12 +12,12 @@
 //     code at bit P: one AND isolates two codes and is all the conversion
 //     there is. Codes are used at several P without a shift; the activations
 //     that meet them carry 2^(Pmax-P) (Positions). Per group,
-//       acc += D (sum q x - z sum x),
-//     with the groups' sums of x made once with the activations. (They came
-//     from one more MMA at first; a legacy m16n8k16 occupies its tensor pipe
-//     for 8 cycles, so that was a third of the pipe's time.) D (fp32) and z are
-//     applied in fp32; 2^(24-Pmax) and the row's power of two return in the
-//     epilogue.
+//       acc += D (sum q x) - (D z) (sum x),
+//     D in fp32; the second product runs over the groups as a contraction of
+//     its own, tf32 MMAs of 4 groups each, with the groups' sums of x made once
+//     with the activations. (As fused multiply-adds on the accumulators it
+//     took 22 instructions per group, a fifth of all at groups of 32.)
+//     2^(24-Pmax) and the row's power of two return in the epilogue.
 //   - The contraction order inside a 32-code block is free as long as both
 //     operands agree: lane t of a quad owns codes 8t..8t+7 (for groups of 16:
 //     4t..4t+3 of both halves), which are consecutive bits of one word (4
@@ -85,7 +85,7 @@ struct Lists {
   int16_t* expert;     // [entries] of an entry: expert, first column, columns
   int16_t* first;
   int16_t* cols;
-  int* sums;           // [2 kWarps + 1] of the scans; the last: entries
+  int* sums;           // [2 kWarps + 1] of the scans; the last: any choice twice
   int entries;
 
   static __host__ __device__ int max_entries(int n, int E) {
@@ -170,12 +170,16 @@ __device__ __forceinline__ void build_lists(Lists& l, const int32_t* ids,
     return;
   }
   for (int e = tid; e < E; e += kThreads) l.tokens[e] = make_uint2(0, 0);
+  if (tid == 0) l.sums[2 * kWarps] = 0;
   __syncthreads();
   for (int p = tid; p < n; p += kThreads) {
     const int e = ids[p], t = p / top_k;
     if (e >= E && err && blockIdx.x == 0) flag_error(err, TTQ_DEVERR_INDEX);
-    if (e >= 0 && e < E)
-      atomicOr(t < 32 ? &l.tokens[e].x : &l.tokens[e].y, 1u << (t & 31));
+    if (e >= 0 && e < E) {
+      const unsigned bit = 1u << (t & 31);
+      if (atomicOr(t < 32 ? &l.tokens[e].x : &l.tokens[e].y, bit) & bit)
+        l.sums[2 * kWarps] = 1;
+    }
   }
   __syncthreads();
   // exclusive sums over the experts, two per thread
@@ -227,15 +231,15 @@ __device__ __forceinline__ void build_lists(Lists& l, const int32_t* ids,
   __syncthreads();
   for (int p = tid; p < n; p += kThreads) {
     const int e = ids[p], t = p / top_k, last = (t + 1) * top_k;
-    bool ok = e >= 0 && e < E;  // the first of equal choices stands for all
-    for (int q = t * top_k; ok && q < p; ++q) ok = ids[q] != e;
-    if (!ok) continue;
-    float w = 0.f;
-    if (weights) {
-      w = weights[p];
-      for (int q = p + 1; q < last; ++q)
-        if (ids[q] == e) w += weights[q];
+    bool ok = e >= 0 && e < E;
+    float w = weights ? weights[p] : 0.f;
+    if (l.sums[2 * kWarps]) {  // the first of equal choices stands for all
+      for (int q = t * top_k; ok && q < p; ++q) ok = ids[q] != e;
+      if (ok && weights)
+        for (int q = p + 1; q < last; ++q)
+          if (ids[q] == e) w += weights[q];
     }
+    if (!ok) continue;
     const uint2 m = l.tokens[e];
     const unsigned below = (1u << (t & 31)) - 1u;
     const int at = l.start[e] + (t < 32 ? __popc(m.x & below)
@@ -477,8 +481,31 @@ __device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0,
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
+// The same from a zero accumulator: no registers to clear first.
+__device__ __forceinline__ void mma_f16_first(float (&c)[4], uint32_t a0,
+                                              uint32_t a1, uint32_t a2,
+                                              uint32_t a3, uint32_t b0,
+                                              uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 "
+      "{%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+      : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
+}
+__device__ __forceinline__ void mma_tf32(float (&c)[4], uint32_t a0,
+                                         uint32_t a1, uint32_t b0) {
+  asm("mma.sync.aligned.m16n8k4.row.col.f32.tf32.tf32.f32 "
+      "{%0,%1,%2,%3}, {%4,%5}, {%6}, {%0,%1,%2,%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a0), "r"(a1), "r"(b0));
+}
+__device__ __forceinline__ uint32_t tf32(float v) {
+  uint32_t r;
+  asm("cvt.rna.tf32.f32 %0, %1;" : "=r"(r) : "f"(v));
+  return r;
+}
+
 // What the kernels do with the activations' precision.
-//   kOne: one fp16 term, for a bf16 Y.
+//   kOne: one fp16 term (11 bits), for a bf16 Y (8 bits).
 //   kTwo: two fp16 terms (22 bits), for an fp16 Y.
 //   kExact: two terms, and z taken from the codes before the MMA, with the
 //     codes as normal numbers, for an fp32 Y: subnormal operands are not
@@ -508,16 +535,13 @@ __device__ __forceinline__ void subtract(uint32_t& p, __half2 z) {
 // instructions apart), otherwise nblocks. xp[n] (and xp[n] + term for the
 // second term) points at the lane's activations of the stage: 16 bytes per
 // 32-channel block, 64 bytes apart, .x and .y for the block's first MMA, .z
-// and .w for its second; xv holds the first block's. sums[n] holds, in lane
-// (g, t), the sum of x of column g's group t of the piece (of 16-channel
-// groups: 2t and 2t + 1).
+// and .w for its second; xv holds the first block's.
 template <int BITS, bool G16, int LG, bool FULL, int MODE, int NT, int NTMAX>
 __device__ __forceinline__ void stage_products(
     const uint8_t* st, const uint8_t* dd, int j0,
     const Field<BITS, G16, MODE == kExact>& f, int nblocks,
     const uint4* const (&xp)[NTMAX], int64_t term,
-    uint4 (&xv)[NTMAX][kTerms<MODE>], const float2 (&sums)[NTMAX],
-    float (&acc)[2][NTMAX][4], int lane) {
+    uint4 (&xv)[NTMAX][kTerms<MODE>], float (&acc)[2][NTMAX][4], int lane) {
   constexpr int TERMS = kTerms<MODE>;
   constexpr bool kCentre = MODE == kExact;
   constexpr int kD = kPieceDelta<G16>;
@@ -543,60 +567,33 @@ __device__ __forceinline__ void stage_products(
       }
     }
   };
-  auto clear = [&]() {
-#pragma unroll
-    for (int n = 0; n < NT; ++n)
-#pragma unroll
-      for (int i = 0; i < 4; ++i) cc[0][n][i] = cc[1][n][i] = 0.f;
-  };
-  // -z in units: 2^23 + z by one OR, and one exact fused multiply-add
-  auto minus_z = [&](int i, int j) -> float {
-    constexpr float u = kUnit<BITS, G16, MODE>;
-    return fmaf(__uint_as_float(0x4B000000u | zero_at(i, j)), -u,
-                8388608.f * u);
-  };
-  // acc += D (c - z s) for group j of the stage
+  // acc += D c for group j of the stage
   auto flush = [&](int j) {
-    float s[NT][2];  // of the lane's accumulator columns 2t, 2t + 1
-    if constexpr (!kCentre) {
-      const int from = 8 * (lane & 3) + (G16 ? j >> 1 : j0 + j);
-#pragma unroll
-      for (int n = 0; n < NT; ++n) {
-        const float v = G16 && (j & 1) ? sums[n].y : sums[n].x;
-        s[n][0] = __shfl_sync(0xffffffffu, v, from);
-        s[n][1] = __shfl_sync(0xffffffffu, v, from + 4);
-      }
-    }
 #pragma unroll
     for (int rt = 0; rt < 2; ++rt) {
       const float d0 = delta_at(2 * rt, j), d1 = delta_at(2 * rt + 1, j);
-      float z0 = 0.f, z1 = 0.f;
-      if constexpr (!kCentre) {
-        z0 = minus_z(2 * rt, j);
-        z1 = minus_z(2 * rt + 1, j);
-      }
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
-        float v[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-          v[i] = kCentre ? cc[rt][n][i]
-                         : fmaf(i < 2 ? z0 : z1, s[n][i & 1], cc[rt][n][i]);
-        acc[rt][n][0] = fmaf(d0, v[0], acc[rt][n][0]);
-        acc[rt][n][1] = fmaf(d0, v[1], acc[rt][n][1]);
-        acc[rt][n][2] = fmaf(d1, v[2], acc[rt][n][2]);
-        acc[rt][n][3] = fmaf(d1, v[3], acc[rt][n][3]);
+        acc[rt][n][0] = fmaf(d0, cc[rt][n][0], acc[rt][n][0]);
+        acc[rt][n][1] = fmaf(d0, cc[rt][n][1], acc[rt][n][1]);
+        acc[rt][n][2] = fmaf(d1, cc[rt][n][2], acc[rt][n][2]);
+        acc[rt][n][3] = fmaf(d1, cc[rt][n][3], acc[rt][n][3]);
       }
     }
   };
+  // first: the group's first MMA
   auto products = [&](const uint32_t (&p)[2][2][4], int h, int n, uint32_t b0,
-                      uint32_t b1) {
+                      uint32_t b1, bool first) {
 #pragma unroll
-    for (int rt = 0; rt < 2; ++rt)
-      mma_f16(cc[rt][n], p[rt][0][2 * h], p[rt][1][2 * h],
-              p[rt][0][2 * h + 1], p[rt][1][2 * h + 1], b0, b1);
+    for (int rt = 0; rt < 2; ++rt) {
+      if (first)
+        mma_f16_first(cc[rt][n], p[rt][0][2 * h], p[rt][1][2 * h],
+                      p[rt][0][2 * h + 1], p[rt][1][2 * h + 1], b0, b1);
+      else
+        mma_f16(cc[rt][n], p[rt][0][2 * h], p[rt][1][2 * h],
+                p[rt][0][2 * h + 1], p[rt][1][2 * h + 1], b0, b1);
+    }
   };
-  clear();
 #pragma unroll
   for (int b = 0; b < 4; ++b) {
     if (FULL || b < nblocks) {
@@ -639,9 +636,8 @@ __device__ __forceinline__ void stage_products(
 #pragma unroll
             for (int k = 0; k < TERMS; ++k)
               products(p, h, n, h ? xv[n][k].z : xv[n][k].x,
-                       h ? xv[n][k].w : xv[n][k].y);
+                       h ? xv[n][k].w : xv[n][k].y, k == 0);
           flush(2 * b + h);
-          clear();
         }
       } else {
 #pragma unroll
@@ -651,17 +647,59 @@ __device__ __forceinline__ void stage_products(
 #pragma unroll
             for (int k = 0; k < TERMS; ++k)
               products(p, h, n, h ? xv[n][k].z : xv[n][k].x,
-                       h ? xv[n][k].w : xv[n][k].y);
-        if (((b + 1) & ((1 << LG) - 1)) == 0) {
-          flush(b >> LG);
-          if (b < 3) clear();
-        }
+                       h ? xv[n][k].w : xv[n][k].y,
+                       h == 0 && k == 0 && (b & ((1 << LG) - 1)) == 0);
+        if (((b + 1) & ((1 << LG) - 1)) == 0) flush(b >> LG);
       }
 #pragma unroll
       for (int n = 0; n < NT; ++n)
 #pragma unroll
         for (int k = 0; k < TERMS; ++k)
           if (kAhead && b < 3) xv[n][k] = xn[n][k];
+    }
+  }
+}
+
+// acc -= (D z) (sum x), both factors in two tf32 terms (z is several times the
+// spread of the codes around it: one term of 11 bits cost a bf16 Y 5e-3), for
+// the groups of a piece (dd) that the warp contracts:
+// group g0 + t (for groups of 16: g0 + 2t and g0 + 2t + 1) of lane (g, t) if
+// it is in [lo, hi). sp[n]: column g's sums.
+template <int BITS, bool G16, int MODE, int NT, int NTMAX>
+__device__ __forceinline__ void zero_products(const uint8_t* dd, int g0,
+                                              int lo, int hi,
+                                              const float* const (&sp)[NTMAX],
+                                              float (&acc)[2][NTMAX][4],
+                                              int lane) {
+  constexpr int kD = kPieceDelta<G16>, kPer = G16 ? 2 : 1;
+  constexpr float u = kUnit<BITS, G16, MODE>;
+  const int g = lane >> 2;
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) {
+    const int j = (lane & 3) * kPer + i;
+    const bool mine = g0 + j >= lo && g0 + j < hi;
+    const uint8_t* dp = dd + g * kD + j * 4;
+    const uint8_t* zp = dd + kRows * kD + g * (kD / 4) + j;
+    float a[4];  // -D z in units of rows g, g + 8, g + 16, g + 24
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      // z as a float: 2^23 + z by one OR
+      const float z =
+          __uint_as_float(0x4B000000u | zp[r * 8 * (kD / 4)]) - 8388608.f;
+      a[r] = mine ? __uint_as_float(word(dp + r * 8 * kD)) * (z * -u) : 0.f;
+    }
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+      const float s = mine ? sp[n][g0 + j] : 0.f;
+      const uint32_t s0 = tf32(s);
+#pragma unroll
+      for (int rt = 0; rt < 2; ++rt) {
+        const uint32_t a0 = tf32(a[2 * rt]), a1 = tf32(a[2 * rt + 1]);
+        mma_tf32(acc[rt][n], a0, a1, s0);
+        mma_tf32(acc[rt][n], tf32(a[2 * rt] - __uint_as_float(a0)),
+                 tf32(a[2 * rt + 1] - __uint_as_float(a1)), s0);
+        mma_tf32(acc[rt][n], a0, a1, tf32(s - __uint_as_float(s0)));
+      }
     }
   }
 }
@@ -703,12 +741,11 @@ struct Tile {
   const Field<BITS, G16, MODE == kExact> f;
   const uint8_t* ring;
   int lane, nt;
-  int stage, piece;        // ring positions: of the next stage, after the last
-                           // piece
+  int stage, piece;        // ring positions of the next ones
   bool fresh;
+  const uint8_t* dd;       // the last piece
   const uint4* xp[NTMAX];  // the lane's activations at the next stage
   const float* sp[NTMAX];  // its column's group sums
-  float2 sums[NTMAX];
   int64_t term;
   float acc[2][NTMAX][4];
 
@@ -740,43 +777,39 @@ struct Tile {
   template <int LG, int NT, typename NF>
   __device__ __forceinline__ void run_nt(const Packed& m, int c, int c_end,
                                          NF&& next) {
+    constexpr int kPer = G16 ? 8 : 4 >> LG;  // groups per chunk
+    const int lo = c * kPer;
+    const int hi = min(c_end * kPer, G16 ? m.blocks * 2 : m.blocks >> LG);
     for (; c < c_end; ++c) {
       uint4 xv[NTMAX][TERMS];
 #pragma unroll
       for (int n = 0; n < NT; ++n)
 #pragma unroll
         for (int k = 0; k < TERMS; ++k) xv[n][k] = xp[n][k * term];
-      cp_async_wait<S - 2>();
-      __syncwarp();  // the stage is there, and every lane has left the last
-      next();
+      cp_async_wait<S - 1>();
+      __syncwarp();  // every lane's part of the stage is there
       if (fresh || m.new_piece(c)) {
+        dd = ring + S * kStage<BITS> + piece * kPiece<G16>;
         piece = piece + 1 == S ? 0 : piece + 1;
         fresh = false;
-        if constexpr (MODE != kExact) {
-#pragma unroll
-          for (int n = 0; n < NT; ++n) {
-            if constexpr (G16)
-              sums[n] = *reinterpret_cast<const float2*>(sp[n] + c * 8 +
-                                                         2 * (lane & 3));
-            else
-              sums[n].x = sp[n][(c >> LG) * 4 + (lane & 3)];
-          }
-        }
+        if constexpr (MODE != kExact)
+          zero_products<BITS, G16, MODE, NT, NTMAX>(
+              dd, G16 ? c * 8 : (c >> LG) * 4, lo, hi, sp, acc, lane);
       }
       const uint8_t* st = ring + stage * kStage<BITS>;
-      const uint8_t* dd = ring + S * kStage<BITS> +
-                          (piece == 0 ? S - 1 : piece - 1) * kPiece<G16>;
       const int j0 = G16 ? 0 : (c * (4 >> LG)) & 3;
       const int nb = m.blocks - 4 * c;
       if (nb >= 4)
         stage_products<BITS, G16, LG, true, MODE, NT, NTMAX>(
-            st, dd, j0, f, 4, xp, term, xv, sums, acc, lane);
+            st, dd, j0, f, 4, xp, term, xv, acc, lane);
       else
         stage_products<BITS, G16, LG, false, MODE, NT, NTMAX>(
-            st, dd, j0, f, nb, xp, term, xv, sums, acc, lane);
+            st, dd, j0, f, nb, xp, term, xv, acc, lane);
 #pragma unroll
       for (int n = 0; n < NT; ++n) xp[n] += 16;
       stage = stage + 1 == S ? 0 : stage + 1;
+      __syncwarp();  // every lane has left the stage
+      next();
     }
   }
   template <int LG, typename NF>
@@ -791,12 +824,13 @@ struct Tile {
 
 // ------------------------------------------------------------------ up ---
 
-// A warp's tile is 16 intermediate channels: their 16 gate rows and the 16
-// rows of the other factor, which end in the same lanes and registers. The
-// CTA's 8 warps are `rs` neighbouring tiles of one entry times 8 / rs parts
-// of K; units (entry, rs tiles) are taken round robin by a persistent grid.
-// Neighbouring tiles share their activations through L1; parts of K are added
-// through shared memory.
+// A tile is 16 intermediate channels of an entry: their 16 gate rows and the
+// 16 rows of the other factor, which end in the same lanes and registers. A CTA
+// of the persistent grid takes an even share of consecutive tiles, and its 8
+// warps even shares of those tiles' chunks, one after the other: a warp that
+// starts a tile and does not end it adds what the warps after it contracted
+// (through shared memory, in order). So all warps do the same number of steps
+// whatever the number of tiles, and one barrier joins them.
 template <int BITS, bool G16, int LG, int MODE, int NTMAX, bool LOCAL>
 __global__ void __launch_bounds__(kThreads, 2)
     up_kernel(const UpArgs a) {
@@ -804,7 +838,7 @@ __global__ void __launch_bounds__(kThreads, 2)
   constexpr int S = TileT::S;
   extern __shared__ __align__(16) uint8_t sm[];
   Lists l(sm, a.T * a.top_k, a.E);
-  float* red =  // [warp][row tile][column tile][128]
+  float* red =  // [warp][row tile][column tile][128]: what ends a tile
       reinterpret_cast<float*>(sm + Lists::bytes(a.T * a.top_k, a.E));
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const uint8_t* ring = reinterpret_cast<const uint8_t*>(
@@ -815,57 +849,43 @@ __global__ void __launch_bounds__(kThreads, 2)
   // ids and the packed weights were complete before the kernel that runs
   // before this one started: lists and the first stages need not wait for it
   build_lists(l, a.ids, nullptr, a.T, a.top_k, a.E, a.err);
-  const int rs = a.rs, ks = kWarps / rs;
-  const int wr = warp % rs, wk = warp / rs;
-  const int tiles = a.I / 16, rows = (tiles + rs - 1) / rs;
+  const int tiles = a.I / 16;  // of an entry
   const int chunks = (a.K + kChunk - 1) / kChunk;
-  const int c0 = wk * chunks / ks, c1 = (wk + 1) * chunks / ks;
+  const int64_t all = (int64_t)l.entries * tiles;
+  const int64_t t0 = all * blockIdx.x / gridDim.x;
+  const int steps =
+      (int)(all * (blockIdx.x + 1) / gridDim.x - t0) * chunks;  // the CTA's
+  const int s0 = (int)((int64_t)steps * warp / kWarps);
+  const int s1 = (int)((int64_t)steps * (warp + 1) / kWarps);
+  // where the warp starts: entry, tile of the entry, chunk
+  const int from = s0 / chunks;
+  const int en0 = (int)((t0 + from) / tiles);
+  const int tile0 = (int)(t0 + from - (int64_t)en0 * tiles);
+  const int c0 = s0 - from * chunks;
   const Packed m(a.codes, a.delta, a.zero, a.K, BITS, a.group);
   Stream<BITS, G16> w(m, a.I, lane);
 
-  // units: (entry, row of rs tiles), a step of gridDim.x at a time
-  struct Unit {
-    int en, row;
+  int left = s1 - s0, ien = en0, itile = tile0;
+  auto seek = [&](int c) {
+    w.seek(m, (int64_t)l.expert[ien] * 2 * a.I + itile * 16, c);
   };
-  const int step_en = gridDim.x / rows, step_row = gridDim.x - step_en * rows;
-  auto next_unit = [&](Unit& u) {
-    u.en += step_en;
-    u.row += step_row;
-    if (u.row >= rows) {
-      u.row -= rows;
-      ++u.en;
-    }
-  };
-  Unit first;
-  first.en = blockIdx.x / rows;
-  first.row = blockIdx.x - first.en * rows;
-  // the warp's stages: its chunks of the CTA's units, one after the other
-  Unit iu = first;
-  auto seek = [&]() {
-    // the warp's tile of unit iu, skipping units in which it has none
-    for (; iu.en < l.entries && c0 < c1; next_unit(iu)) {
-      const int tile = iu.row * rs + wr;
-      if (tile < tiles) {
-        w.seek(m, (int64_t)l.expert[iu.en] * 2 * a.I + tile * 16, c0);
-        return;
-      }
-    }
-    iu.en = l.entries;
-  };
+  if (left > 0) seek(c0);
   auto issue = [&]() {
-    if (iu.en < l.entries) {
+    if (left > 0) {
       w.copy(m, ring_at, lane);
-      if (w.c == c1) {
-        next_unit(iu);
-        seek();
+      if (--left > 0 && w.c == chunks) {
+        if (++itile == tiles) {
+          itile = 0;
+          ++ien;
+        }
+        seek(0);
       }
     }
     cp_async_commit();
     w.advance();
   };
-  seek();
 #pragma unroll
-  for (int i = 0; i < S - 1; ++i) issue();
+  for (int i = 0; i < S; ++i) issue();
   griddep_enter();
 
   const uint4* xhat = a.xhat;
@@ -893,70 +913,86 @@ __global__ void __launch_bounds__(kThreads, 2)
     xmax = mx;
   }
   TileT tl(ring, lane, (int64_t)a.T * a.K / 8);
-  for (Unit u = first; u.en < l.entries; next_unit(u)) {
-    const int en = u.en, tile = u.row * rs + wr;
+  // h of a finished tile
+  auto finish = [&](int en, int tile) {
+    constexpr float per_unit = 1.f / kUnit<BITS, G16, MODE>;
+    constexpr int most = MODE == kExact ? 0 : Positions<BITS, G16>::kMost;
     const int cols = l.cols[en], col0 = l.first[en];
-    const bool live = tile < tiles;
-    tl.start(m, xhat, xsum, cols, c0,
-             [&](int col) { return (int64_t)l.token[col0 + col]; });
-    if (live) tl.template run<LG>(m, c0, c1, issue);
-    if (ks > 1) {
-      // parts of K to the warp of part 0
-      __syncthreads();  // the last sums have been read
-      if (wk > 0) {
+    const int ch = tile * 16 + (lane >> 2);
+    const float* mid = a.inv_s_mid + (int64_t)l.expert[en] * a.I + ch;
+    const float mid0 = mid[0], mid1 = mid[8];
 #pragma unroll
-        for (int rt = 0; rt < 2; ++rt)
+    for (int n = 0; n < NTMAX; ++n) {
+      if (n >= tl.nt) break;
 #pragma unroll
-          for (int n = 0; n < NTMAX; ++n)
-            *reinterpret_cast<float4*>(
-                red + ((warp * 2 + rt) * NTMAX + n) * 128 + lane * 4) =
-                make_float4(tl.acc[rt][n][0], tl.acc[rt][n][1],
-                            tl.acc[rt][n][2], tl.acc[rt][n][3]);
-      }
-      __syncthreads();
-      if (wk == 0) {
-        for (int k = 1; k < ks; ++k) {
-          const int from = k * rs + wr;
-#pragma unroll
-          for (int rt = 0; rt < 2; ++rt)
-#pragma unroll
-            for (int n = 0; n < NTMAX; ++n) {
-              const float4 v = *reinterpret_cast<const float4*>(
-                  red + ((from * 2 + rt) * NTMAX + n) * 128 + lane * 4);
-              tl.acc[rt][n][0] += v.x;
-              tl.acc[rt][n][1] += v.y;
-              tl.acc[rt][n][2] += v.z;
-              tl.acc[rt][n][3] += v.w;
-            }
+      for (int i = 0; i < 2; ++i) {
+        const int col = n * 8 + 2 * (lane & 3) + i;
+        if (col < cols) {
+          const int slot = l.slot[col0 + col];
+          const float un = row_unscale(xmax[l.token[col0 + col]], most);
+          float* h = a.h + (int64_t)slot * a.I + ch;
+          h[0] = gated(tl.acc[0][n][i] * per_unit * un, a.act) *
+                 (tl.acc[1][n][i] * per_unit * un) * mid0;
+          h[8] = gated(tl.acc[0][n][2 + i] * per_unit * un, a.act) *
+                 (tl.acc[1][n][2 + i] * per_unit * un) * mid1;
         }
       }
     }
-    if (wk == 0 && live) {
-      constexpr float per_unit = 1.f / kUnit<BITS, G16, MODE>;
-      constexpr int most = MODE == kExact ? 0 : Positions<BITS, G16>::kMost;
-      const int ch = tile * 16 + (lane >> 2);
-      const float* mid = a.inv_s_mid + (int64_t)l.expert[en] * a.I + ch;
-      const float mid0 = mid[0], mid1 = mid[8];
+  };
+  int s = s0, en = en0, tile = tile0, c = c0;
+  bool open = false;  // the last tile goes on in the next warp
+  while (s < s1) {
+    const int col0 = l.first[en];
+    tl.start(m, xhat, xsum, l.cols[en], c,
+             [&](int col) { return (int64_t)l.token[col0 + col]; });
+    const int stop = min(s1, s + chunks - c);
+    const bool ends = stop - s == chunks - c;
+    tl.template run<LG>(m, c, c + stop - s, issue);
+    s = stop;
+    if (c > 0) {  // the warp before started it
 #pragma unroll
-      for (int n = 0; n < NTMAX; ++n) {
-        if (n >= tl.nt) break;
+      for (int rt = 0; rt < 2; ++rt)
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const int col = n * 8 + 2 * (lane & 3) + i;
-          if (col < cols) {
-            const int slot = l.slot[col0 + col];
-            const float un = row_unscale(xmax[l.token[col0 + col]], most);
-            float* h = a.h + (int64_t)slot * a.I + ch;
-            h[0] = gated(tl.acc[0][n][i] * per_unit * un, a.act) *
-                   (tl.acc[1][n][i] * per_unit * un) * mid0;
-            h[8] = gated(tl.acc[0][n][2 + i] * per_unit * un, a.act) *
-                   (tl.acc[1][n][2 + i] * per_unit * un) * mid1;
-          }
-        }
-      }
+        for (int n = 0; n < NTMAX; ++n)
+          *reinterpret_cast<float4*>(
+              red + ((warp * 2 + rt) * NTMAX + n) * 128 + lane * 4) =
+              make_float4(tl.acc[rt][n][0], tl.acc[rt][n][1],
+                          tl.acc[rt][n][2], tl.acc[rt][n][3]);
+    } else if (ends) {
+      finish(en, tile);
+    } else {
+      open = true;
+      break;
+    }
+    c = 0;
+    if (ends && ++tile == tiles) {
+      tile = 0;
+      ++en;
     }
   }
   cp_async_wait_all();
+  __syncthreads();
+  if (open) {
+    // the tile ends chunks - (steps the warp did) after s1
+    const int start = s1 / chunks * chunks;  // the tile's first step
+    for (int k = warp + 1; k < kWarps; ++k) {
+      const int from_k = (int)((int64_t)steps * k / kWarps);
+      if (from_k >= start + chunks) break;
+      if (from_k == (int)((int64_t)steps * (k + 1) / kWarps)) continue;
+#pragma unroll
+      for (int rt = 0; rt < 2; ++rt)
+#pragma unroll
+        for (int n = 0; n < NTMAX; ++n) {
+          const float4 v = *reinterpret_cast<const float4*>(
+              red + ((k * 2 + rt) * NTMAX + n) * 128 + lane * 4);
+          tl.acc[rt][n][0] += v.x;
+          tl.acc[rt][n][1] += v.y;
+          tl.acc[rt][n][2] += v.z;
+          tl.acc[rt][n][3] += v.w;
+        }
+    }
+    finish(en, tile);
+  }
 }
 
 // ---------------------------------------------------------------- down ---
@@ -1015,7 +1051,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     w.advance();
   };
 #pragma unroll
-  for (int i = 0; i < S - 1; ++i) issue();
+  for (int i = 0; i < S; ++i) issue();
   griddep_enter();
 
   const uint4* hhat = a.hhat;
@@ -1128,22 +1164,6 @@ bool allow_smem(K kern, size_t bytes) {
                               (int)bytes) == cudaSuccess;
 }
 
-// The rows a CTA's warps share out. More neighbouring tiles read an
-// activation once for more weights; fewer leave finer units to balance. Time
-// goes with rounds x rs; the largest rs within 10% of the best is taken.
-inline int pick_rs(int64_t tiles, int64_t slots) {
-  int64_t best = INT64_MAX;
-  for (int rs = 1; rs <= kWarps; rs *= 2) {
-    const int64_t units = (tiles + rs - 1) / rs;
-    best = std::min(best, (units + slots - 1) / slots * rs);
-  }
-  for (int rs = kWarps; rs > 1; rs /= 2) {
-    const int64_t units = (tiles + rs - 1) / rs;
-    if ((units + slots - 1) / slots * rs * 10 <= best * 11) return rs;
-  }
-  return 1;
-}
-
 inline int ctas_per_sm(size_t smem) { return smem + 1024 <= 114 * 1024 ? 2 : 1; }
 
 template <int BITS, bool G16, int LG, int MODE, int NTMAX, bool LOCAL>
@@ -1155,7 +1175,6 @@ ttq_status launch_up(UpArgs u, cudaStream_t st) {
   const int64_t slots = ctas_per_sm(ls.smem) * sm_count();
   const int64_t tiles =
       (int64_t)Lists::max_entries(u.T * u.top_k, u.E) * (u.I / 16);
-  u.rs = pick_rs(tiles, slots);
   ls.grid = dim3((unsigned)std::min<int64_t>(tiles, slots));
   auto kern = up_kernel<BITS, G16, LG, MODE, NTMAX, LOCAL>;
   if (!allow_smem(kern, ls.smem)) return TTQ_ERR_CUDA;
