@@ -491,17 +491,22 @@ __device__ __forceinline__ void mma_f16_first(float (&c)[4], uint32_t a0,
       : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
 }
-__device__ __forceinline__ void mma_tf32(float (&c)[4], uint32_t a0,
-                                         uint32_t a1, uint32_t b0) {
-  asm("mma.sync.aligned.m16n8k4.row.col.f32.tf32.tf32.f32 "
-      "{%0,%1,%2,%3}, {%4,%5}, {%6}, {%0,%1,%2,%3};"
+// Two tf32 contractions over 4 positions each: a0, a1 (rows g, g + 8) with b0
+// and a2, a3 with b1.
+__device__ __forceinline__ void mma_tf32(float (&c)[4], float a0, float a1,
+                                         float a2, float a3, float b0,
+                                         float b1) {
+  asm("mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 "
+      "{%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-      : "r"(a0), "r"(a1), "r"(b0));
+      : "r"(__float_as_uint(a0)), "r"(__float_as_uint(a1)),
+        "r"(__float_as_uint(a2)), "r"(__float_as_uint(a3)),
+        "r"(__float_as_uint(b0)), "r"(__float_as_uint(b1)));
 }
-__device__ __forceinline__ uint32_t tf32(float v) {
-  uint32_t r;
-  asm("cvt.rna.tf32.f32 %0, %1;" : "=r"(r) : "f"(v));
-  return r;
+// The first 11 bits of v, which tf32 holds; the MMA cuts the rest of what it
+// is given in the same way.
+__device__ __forceinline__ float tf32_head(float v) {
+  return __uint_as_float(__float_as_uint(v) & 0xFFFFE000u);
 }
 
 // What the kernels do with the activations' precision.
@@ -664,10 +669,10 @@ __device__ __forceinline__ void stage_products(
 // spread of the codes around it: one term of 11 bits cost a bf16 Y 5e-3), for
 // the groups of a piece (dd) that the warp contracts:
 // group g0 + t (for groups of 16: g0 + 2t and g0 + 2t + 1) of lane (g, t) if
-// it is in [lo, hi). sp[n]: column g's sums.
+// it is in [lo, hi); g0 + j1 is one that is. sp[n]: column g's sums.
 template <int BITS, bool G16, int MODE, int NT, int NTMAX>
 __device__ __forceinline__ void zero_products(const uint8_t* dd, int g0,
-                                              int lo, int hi,
+                                              int j1, int lo, int hi,
                                               const float* const (&sp)[NTMAX],
                                               float (&acc)[2][NTMAX][4],
                                               int lane) {
@@ -676,29 +681,32 @@ __device__ __forceinline__ void zero_products(const uint8_t* dd, int g0,
   const int g = lane >> 2;
 #pragma unroll
   for (int i = 0; i < kPer; ++i) {
-    const int j = (lane & 3) * kPer + i;
-    const bool mine = g0 + j >= lo && g0 + j < hi;
+    const int at = (lane & 3) * kPer + i;
+    const bool mine = g0 + at >= lo && g0 + at < hi;
+    const int j = mine ? at : j1;  // what lies outside may not be a number
     const uint8_t* dp = dd + g * kD + j * 4;
     const uint8_t* zp = dd + kRows * kD + g * (kD / 4) + j;
-    float a[4];  // -D z in units of rows g, g + 8, g + 16, g + 24
+    float a[4], b[4];  // -D z in units of rows g, g + 8, ..: head, tail
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
-      // z as a float: 2^23 + z by one OR
+      // -z in units: 2^23 + z by one OR, and one exact fused multiply-add
       const float z =
-          __uint_as_float(0x4B000000u | zp[r * 8 * (kD / 4)]) - 8388608.f;
-      a[r] = mine ? __uint_as_float(word(dp + r * 8 * kD)) * (z * -u) : 0.f;
+          fmaf(__uint_as_float(0x4B000000u | zp[r * 8 * (kD / 4)]), -u,
+               8388608.f * u);
+      const float v = __uint_as_float(word(dp + r * 8 * kD)) * z;
+      a[r] = tf32_head(v);
+      b[r] = v - a[r];
     }
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
       const float s = mine ? sp[n][g0 + j] : 0.f;
-      const uint32_t s0 = tf32(s);
+      const float s0 = tf32_head(s), s1 = s - s0;
 #pragma unroll
       for (int rt = 0; rt < 2; ++rt) {
-        const uint32_t a0 = tf32(a[2 * rt]), a1 = tf32(a[2 * rt + 1]);
-        mma_tf32(acc[rt][n], a0, a1, s0);
-        mma_tf32(acc[rt][n], tf32(a[2 * rt] - __uint_as_float(a0)),
-                 tf32(a[2 * rt + 1] - __uint_as_float(a1)), s0);
-        mma_tf32(acc[rt][n], a0, a1, tf32(s - __uint_as_float(s0)));
+        mma_tf32(acc[rt][n], a[2 * rt], a[2 * rt + 1], b[2 * rt],
+                 b[2 * rt + 1], s0, s0);
+        mma_tf32(acc[rt][n], a[2 * rt], a[2 * rt + 1], b[2 * rt],
+                 b[2 * rt + 1], s1, s1);
       }
     }
   }
@@ -794,7 +802,8 @@ struct Tile {
         fresh = false;
         if constexpr (MODE != kExact)
           zero_products<BITS, G16, MODE, NT, NTMAX>(
-              dd, G16 ? c * 8 : (c >> LG) * 4, lo, hi, sp, acc, lane);
+              dd, G16 ? c * 8 : (c >> LG) * 4, G16 ? 0 : (c * (4 >> LG)) & 3,
+              lo, hi, sp, acc, lane);
       }
       const uint8_t* st = ring + stage * kStage<BITS>;
       const int j0 = G16 ? 0 : (c * (4 >> LG)) & 3;
@@ -851,16 +860,17 @@ __global__ void __launch_bounds__(kThreads, 2)
   build_lists(l, a.ids, nullptr, a.T, a.top_k, a.E, a.err);
   const int tiles = a.I / 16;  // of an entry
   const int chunks = (a.K + kChunk - 1) / kChunk;
-  const int64_t all = (int64_t)l.entries * tiles;
-  const int64_t t0 = all * blockIdx.x / gridDim.x;
-  const int steps =
-      (int)(all * (blockIdx.x + 1) / gridDim.x - t0) * chunks;  // the CTA's
-  const int s0 = (int)((int64_t)steps * warp / kWarps);
-  const int s1 = (int)((int64_t)steps * (warp + 1) / kWarps);
+  // the CTA's tiles t0 .. (the first `rest` CTAs take one more) and steps
+  const unsigned all = (unsigned)l.entries * tiles;
+  const unsigned each = all / gridDim.x, rest = all - each * gridDim.x;
+  const unsigned t0 = each * blockIdx.x + min(blockIdx.x, rest);
+  const unsigned steps = (each + (blockIdx.x < rest ? 1 : 0)) * chunks;
+  auto share = [&](int w) { return (int)(steps * w / kWarps); };
+  const int s0 = share(warp), s1 = share(warp + 1);
   // where the warp starts: entry, tile of the entry, chunk
   const int from = s0 / chunks;
-  const int en0 = (int)((t0 + from) / tiles);
-  const int tile0 = (int)(t0 + from - (int64_t)en0 * tiles);
+  const int en0 = (int)((t0 + from) / (unsigned)tiles);
+  const int tile0 = (int)(t0 + from) - en0 * tiles;
   const int c0 = s0 - from * chunks;
   const Packed m(a.codes, a.delta, a.zero, a.K, BITS, a.group);
   Stream<BITS, G16> w(m, a.I, lane);
@@ -976,9 +986,8 @@ __global__ void __launch_bounds__(kThreads, 2)
     // the tile ends chunks - (steps the warp did) after s1
     const int start = s1 / chunks * chunks;  // the tile's first step
     for (int k = warp + 1; k < kWarps; ++k) {
-      const int from_k = (int)((int64_t)steps * k / kWarps);
-      if (from_k >= start + chunks) break;
-      if (from_k == (int)((int64_t)steps * (k + 1) / kWarps)) continue;
+      if (share(k) >= start + chunks) break;
+      if (share(k) == share(k + 1)) continue;
 #pragma unroll
       for (int rt = 0; rt < 2; ++rt)
 #pragma unroll
@@ -1030,8 +1039,8 @@ __global__ void __launch_bounds__(kThreads, 2)
   const int total = tile * kRows < a.K ? l.entries * chunks : 0;
   const int ranks = gridDim.y, rank = blockIdx.y;
   const int parts = ranks * ks, part = rank * ks + wk;
-  const int s0 = (int)((int64_t)total * part / parts);
-  const int s1 = (int)((int64_t)total * (part + 1) / parts);
+  const int s0 = (int)((unsigned)total * part / parts);
+  const int s1 = (int)((unsigned)total * (part + 1) / parts);
   const Packed m(a.codes, a.delta, a.zero, a.I, BITS, a.group);
   Stream<BITS, G16> w(m, 16, lane);
   int is = s0, ien = s0 / chunks;
