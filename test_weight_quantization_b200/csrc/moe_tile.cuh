@@ -58,15 +58,19 @@ template <bool G16>
 constexpr int kPiece = kRows * (kPieceDelta<G16> + kPieceDelta<G16> / 4);
 // Stages per warp: what lets two CTAs of 8 warps share an SM. As many pieces:
 // a stage needs at most one new one.
-template <int BITS>
-constexpr int kStages = BITS <= 3 ? 5 : BITS <= 5 ? 3 : 2;
-template <int BITS, bool G16>
-constexpr int kRing = kStages<BITS> * (kStage<BITS> + kPiece<G16>);
+#ifndef TTQ_S2
+#define TTQ_S2 2
+#endif
+template <int BITS, int NTMAX>
+constexpr int kStages = NTMAX == 1 ? (BITS <= 3 ? 5 : BITS <= 5 ? 3 : 2)
+                                   : (BITS <= 3 ? TTQ_S2 + 1 : BITS <= 5 ? TTQ_S2 : 2);
+template <int BITS, bool G16, int NTMAX>
+constexpr int kRing = kStages<BITS, NTMAX> * (kStage<BITS> + kPiece<G16>);
 // Where the rows a CTA converts itself start: after the rings, which start at
 // byte `ring`.
-template <int BITS, bool G16>
+template <int BITS, bool G16, int NTMAX>
 constexpr int smem_rows(int ring) {
-  return ring + 8 * kRing<BITS, G16>;
+  return ring + 8 * kRing<BITS, G16, NTMAX>;
 }
 
 // ------------------------------------------------------------- columns ---
@@ -290,7 +294,7 @@ struct Packed {
 // A lane's share of the copies of 32 rows: the tile's rows 0..15 are
 // consecutive matrix rows, 16..31 start `skip` rows after the first. Offsets
 // are bytes from the tile's first row; an expert's matrix is below 2^31 bytes.
-template <int BITS, bool G16>
+template <int BITS, bool G16, int S>
 struct Stream {
   uint32_t code_off[BITS];  // the lane's 16-byte pieces of the codes
   uint32_t row_off;         // entries from the first row to the lane's row
@@ -346,7 +350,7 @@ struct Stream {
     // The pitch of delta and zero is a multiple of 16 entries: a piece is
     // always there.
     if (fresh || m.new_piece(c)) {
-      constexpr int S = kStages<BITS>, kD = kPieceDelta<G16>;
+      constexpr int kD = kPieceDelta<G16>;
       const uint32_t dd = ring + S * kStage<BITS> + piece * kPiece<G16>;
       if constexpr (G16) {
         cp_async_16(dd + lane * kD, delta + c * 8);
@@ -364,7 +368,7 @@ struct Stream {
     ++c;
   }
   __device__ __forceinline__ void advance() {
-    stage = stage + 1 == kStages<BITS> ? 0 : stage + 1;
+    stage = stage + 1 == S ? 0 : stage + 1;
   }
 };
 
@@ -745,7 +749,7 @@ __device__ __forceinline__ float row_unscale(uint32_t max_bits, int most) {
 template <int BITS, bool G16, int MODE, int NTMAX>
 struct Tile {
   static constexpr int TERMS = kTerms<MODE>;
-  static constexpr int S = kStages<BITS>;
+  static constexpr int S = kStages<BITS, NTMAX>;
   const Field<BITS, G16, MODE == kExact> f;
   const uint8_t* ring;
   int lane, nt;
@@ -835,8 +839,10 @@ struct Tile {
 
 // A tile is 16 intermediate channels of an entry: their 16 gate rows and the
 // 16 rows of the other factor, which end in the same lanes and registers. A CTA
-// of the persistent grid takes an even share of consecutive tiles, and its 8
-// warps even shares of those tiles' chunks, one after the other: a warp that
+// of the persistent grid takes an even share of consecutive tiles. Rounds of 8
+// tiles, one per warp, come first: the warps are then at about the same
+// channels of the same tokens and share their activations through L1. What is
+// left (fewer than 8 tiles) is cut into 8 even runs of chunks: a warp that
 // starts a tile and does not end it adds what the warps after it contracted
 // (through shared memory, in order). So all warps do the same number of steps
 // whatever the number of tiles, and one barrier joins them.
@@ -852,7 +858,7 @@ __global__ void __launch_bounds__(kThreads, 2)
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const uint8_t* ring = reinterpret_cast<const uint8_t*>(
                             red + kWarps * 2 * NTMAX * 128) +
-                        warp * kRing<BITS, G16>;
+                        warp * kRing<BITS, G16, NTMAX>;
   const uint32_t ring_at = smem_u32(ring);
 
   // ids and the packed weights were complete before the kernel that runs
@@ -864,30 +870,44 @@ __global__ void __launch_bounds__(kThreads, 2)
   const unsigned all = (unsigned)l.entries * tiles;
   const unsigned each = all / gridDim.x, rest = all - each * gridDim.x;
   const unsigned t0 = each * blockIdx.x + min(blockIdx.x, rest);
-  const unsigned steps = (each + (blockIdx.x < rest ? 1 : 0)) * chunks;
+  const int mine = each + (blockIdx.x < rest ? 1 : 0);
+  const int rounds = mine / kWarps;
+  // the runs: steps of the tiles from t1 on
+  const unsigned t1 = t0 + rounds * kWarps;
+  const unsigned steps = (mine - rounds * kWarps) * chunks;
   auto share = [&](int w) { return (int)(steps * w / kWarps); };
   const int s0 = share(warp), s1 = share(warp + 1);
-  // where the warp starts: entry, tile of the entry, chunk
-  const int from = s0 / chunks;
-  const int en0 = (int)((t0 + from) / (unsigned)tiles);
-  const int tile0 = (int)(t0 + from) - en0 * tiles;
-  const int c0 = s0 - from * chunks;
   const Packed m(a.codes, a.delta, a.zero, a.K, BITS, a.group);
-  Stream<BITS, G16> w(m, a.I, lane);
+  Stream<BITS, G16, S> w(m, a.I, lane);
 
-  int left = s1 - s0, ien = en0, itile = tile0;
+  int iround = 0, left = s1 - s0;
+  unsigned itile = 0;  // of the whole list
   auto seek = [&](int c) {
-    w.seek(m, (int64_t)l.expert[ien] * 2 * a.I + itile * 16, c);
+    const unsigned en = itile / (unsigned)tiles;
+    w.seek(m, (int64_t)l.expert[en] * 2 * a.I + (itile - en * tiles) * 16, c);
   };
-  if (left > 0) seek(c0);
+  auto seek_first = [&]() {  // of a round, or of the run
+    if (iround < rounds) {
+      itile = t0 + iround * kWarps + warp;
+      seek(0);
+    } else if (left > 0) {
+      const unsigned q = s0 / chunks;
+      itile = t1 + q;
+      seek(s0 - q * chunks);
+    }
+  };
+  seek_first();
   auto issue = [&]() {
-    if (left > 0) {
+    if (iround < rounds) {
+      w.copy(m, ring_at, lane);
+      if (w.c == chunks) {
+        ++iround;
+        seek_first();
+      }
+    } else if (left > 0) {
       w.copy(m, ring_at, lane);
       if (--left > 0 && w.c == chunks) {
-        if (++itile == tiles) {
-          itile = 0;
-          ++ien;
-        }
+        ++itile;
         seek(0);
       }
     }
@@ -902,7 +922,7 @@ __global__ void __launch_bounds__(kThreads, 2)
   const float* xsum = a.xsum;
   const uint32_t* xmax = a.xmax;
   if constexpr (LOCAL) {
-    uint4* x = reinterpret_cast<uint4*>(sm + smem_rows<BITS, G16>(
+    uint4* x = reinterpret_cast<uint4*>(sm + smem_rows<BITS, G16, NTMAX>(
         (int)(reinterpret_cast<const uint8_t*>(red) - sm) +
         kWarps * 2 * NTMAX * 128 * 4));
     float* sum = reinterpret_cast<float*>(
@@ -949,16 +969,28 @@ __global__ void __launch_bounds__(kThreads, 2)
       }
     }
   };
-  int s = s0, en = en0, tile = tile0, c = c0;
+  unsigned en = 0, tile = 0;
   bool open = false;  // the last tile goes on in the next warp
-  while (s < s1) {
+  for (int r = 0, s = s0; r < rounds || s < s1;) {
+    // chunks c .. c_end - 1 of tile `at` of the list
+    unsigned at;
+    int c = 0, c_end = chunks;
+    if (r < rounds) {
+      at = t0 + r * kWarps + warp;
+      ++r;
+    } else {
+      const int q = s / chunks;
+      at = t1 + q;
+      c = s - q * chunks;
+      c_end = min(chunks, c + s1 - s);
+      s += c_end - c;
+    }
+    en = at / (unsigned)tiles;
+    tile = at - en * tiles;
     const int col0 = l.first[en];
     tl.start(m, xhat, xsum, l.cols[en], c,
              [&](int col) { return (int64_t)l.token[col0 + col]; });
-    const int stop = min(s1, s + chunks - c);
-    const bool ends = stop - s == chunks - c;
-    tl.template run<LG>(m, c, c + stop - s, issue);
-    s = stop;
+    tl.template run<LG>(m, c, c_end, issue);
     if (c > 0) {  // the warp before started it
 #pragma unroll
       for (int rt = 0; rt < 2; ++rt)
@@ -968,16 +1000,10 @@ __global__ void __launch_bounds__(kThreads, 2)
               red + ((warp * 2 + rt) * NTMAX + n) * 128 + lane * 4) =
               make_float4(tl.acc[rt][n][0], tl.acc[rt][n][1],
                           tl.acc[rt][n][2], tl.acc[rt][n][3]);
-    } else if (ends) {
+    } else if (c_end == chunks) {
       finish(en, tile);
     } else {
       open = true;
-      break;
-    }
-    c = 0;
-    if (ends && ++tile == tiles) {
-      tile = 0;
-      ++en;
     }
   }
   cp_async_wait_all();
@@ -1024,7 +1050,7 @@ __global__ void __launch_bounds__(kThreads, 2)
   const int region = a.T * kRows;
   const uint8_t* ring =
       reinterpret_cast<const uint8_t*>(ysum + kWarps * region) +
-      warp * kRing<BITS, G16>;
+      warp * kRing<BITS, G16, NTMAX>;
   const uint32_t ring_at = smem_u32(ring);
   float* mine = ysum + warp * region;
 
@@ -1042,7 +1068,7 @@ __global__ void __launch_bounds__(kThreads, 2)
   const int s0 = (int)((unsigned)total * part / parts);
   const int s1 = (int)((unsigned)total * (part + 1) / parts);
   const Packed m(a.codes, a.delta, a.zero, a.I, BITS, a.group);
-  Stream<BITS, G16> w(m, 16, lane);
+  Stream<BITS, G16, S> w(m, 16, lane);
   int is = s0, ien = s0 / chunks;
   auto seek = [&](int c) {
     w.seek(m, (int64_t)l.expert[ien] * a.K + tile * kRows, c);
@@ -1068,7 +1094,7 @@ __global__ void __launch_bounds__(kThreads, 2)
   const uint32_t* hmax = a.hmax;
   const int slots = a.T * a.top_k;
   if constexpr (LOCAL) {
-    uint4* x = reinterpret_cast<uint4*>(sm + smem_rows<BITS, G16>(
+    uint4* x = reinterpret_cast<uint4*>(sm + smem_rows<BITS, G16, NTMAX>(
         (int)(reinterpret_cast<const uint8_t*>(ysum) - sm) +
         kWarps * region * 4));
     float* sum =
@@ -1155,15 +1181,15 @@ __global__ void __launch_bounds__(kThreads, 2)
 
 // -------------------------------------------------------------- launch ---
 
-template <int BITS, bool G16>
-size_t up_smem(int ntmax, int n, int E) {
-  return Lists::bytes(n, E) + (size_t)kWarps * 2 * ntmax * 128 * 4 +
-         (size_t)kWarps * kRing<BITS, G16>;
+template <int BITS, bool G16, int NTMAX>
+size_t up_smem(int n, int E) {
+  return Lists::bytes(n, E) + (size_t)kWarps * 2 * NTMAX * 128 * 4 +
+         (size_t)kWarps * kRing<BITS, G16, NTMAX>;
 }
-template <int BITS, bool G16>
+template <int BITS, bool G16, int NTMAX>
 size_t down_smem(int T, int n, int E) {
   return Lists::bytes(n, E) + (size_t)kWarps * T * kRows * 4 +
-         (size_t)kWarps * kRing<BITS, G16>;
+         (size_t)kWarps * kRing<BITS, G16, NTMAX>;
 }
 
 template <typename K>
@@ -1179,7 +1205,7 @@ template <int BITS, bool G16, int LG, int MODE, int NTMAX, bool LOCAL>
 ttq_status launch_up(UpArgs u, cudaStream_t st) {
   LaunchShape ls;
   ls.block = dim3(kThreads);
-  ls.smem = up_smem<BITS, G16>(NTMAX, u.T * u.top_k, u.E);
+  ls.smem = up_smem<BITS, G16, NTMAX>(u.T * u.top_k, u.E);
   if (LOCAL) ls.smem += rows_bytes(u.T, u.K, u.group, u.format.terms) + 32;
   const int64_t slots = ctas_per_sm(ls.smem) * sm_count();
   const int64_t tiles =
@@ -1194,7 +1220,7 @@ template <int BITS, bool G16, int LG, int MODE, int NTMAX, bool LOCAL>
 ttq_status launch_down(DownArgs d, cudaStream_t st) {
   LaunchShape ls;
   ls.block = dim3(kThreads);
-  ls.smem = down_smem<BITS, G16>(d.T, d.T * d.top_k, d.E);
+  ls.smem = down_smem<BITS, G16, NTMAX>(d.T, d.T * d.top_k, d.E);
   if (LOCAL)
     ls.smem += rows_bytes(d.T * d.top_k, d.I, d.group, d.format.terms) + 32;
   const int slots = ctas_per_sm(ls.smem) * sm_count();
