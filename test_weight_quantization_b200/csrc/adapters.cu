@@ -126,8 +126,11 @@ __global__ void __launch_bounds__(kPlanThreads)
 //   2. out = Y + scale U B^T: tokens as M, 32 output channels as four tiles of
 //      8 whose columns are dealt so that a lane ends with 8 consecutive
 //      channels of its tokens: Y is read and written 16 bytes at a time. The
-//      cluster's warps split N; the first channels' B and Y are on their way
-//      while U is being added up.
+//      cluster's warps split N. With 16-bit types and whole 16-byte rows, B and
+//      Y arrive by cp.async in a ring of units of the warp's own, the
+//      first of them while U is being added up (loads into registers one unit
+//      ahead left the warps waiting 6.7 of 9 cycles per instruction);
+//      otherwise straight into registers.
 // U stays fp32 until it enters step 2, in two 16-bit terms (fp16 ones with a
 // power of two per token, since U may leave fp16's range) or three bf16 terms
 // for fp32. Bound by HBM: X once, Y once in and once out, A and B once per
@@ -162,7 +165,8 @@ struct AddArgs {
   TY* out;
   int64_t ldx, ldy, ldo;
   int T, K, L, r, N, tiles_max;
-  bool vec;  // rows of Y and out on 16-byte boundaries
+  bool vec;   // rows of Y and out on 16-byte boundaries
+  bool ring;  // B and Y through the ring
   uint32_t* err;
 };
 
@@ -182,8 +186,24 @@ constexpr size_t smem_bytes() {
          kTile * 4;
 }
 
+// The ring of step 2: units of up to 32 token rows x 64 bytes of Y and 32 rows
+// of B.
+template <int MT>
+constexpr int kStages = MT == 1 ? 3 : 2;  // two CTAs' worth of shared memory
+template <typename TX, typename TY>
+constexpr bool kRingTypes = sizeof(TX) == 2 && sizeof(TY) == 2;
+template <int MT>
+constexpr int kUnitBytes = kTile * 64 + kCols * MT * 32;
+
+__device__ __forceinline__ void cp_async_16(uint32_t dst, const void* src,
+                                            int bytes) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst),
+               "l"(src), "r"(bytes)
+               : "memory");
+}
+
 // NT: tiles of 8 tokens (1 or 4).
-template <typename TX, typename TY, int MT, int NT>
+template <typename TX, typename TY, int MT, int NT, bool RING>
 __device__ __forceinline__ void add_tile(const AddArgs<TX, TY>& a, int4 tl,
                                          const int32_t* order, int rank,
                                          int ranks, float* sm) {
@@ -309,7 +329,47 @@ __device__ __forceinline__ void add_tile(const AddArgs<TX, TY>& a, int4 tl,
       }
   };
   Unit cur;
-  if (part < units) fetch(part, cur);
+  // the ring: the lane's share of a unit's copies
+  uint8_t* ring = reinterpret_cast<uint8_t*>(sm) + smem_bytes<TX, MT>() +
+                  warp * kStages<MT> * kUnitBytes<MT>;
+  const TY* yr[TM * 2];  // its rows of Y, 8 rows per copy, 8 channels per lane
+  if constexpr (RING) {
+#pragma unroll
+    for (int i = 0; i < TM * 2; ++i) {
+      const int row = i * 8 + g;
+      yr[i] = a.Y + (int64_t)order[row < tl.z ? row : 0] * a.ldy + 8 * t;
+    }
+  }
+  auto issue = [&](int u, int slot) {
+    if constexpr (RING) {
+      if (u < units) {
+        const uint32_t at = smem_u32(ring + slot * kUnitBytes<MT>);
+        const int n0 = u * kCols;
+        // what a row of Y holds from the lane's channel on
+        const int yb = min(16, (a.N - n0 - 8 * t) * 2);
+#pragma unroll
+        for (int i = 0; i < TM * 2; ++i)
+          if (i * 8 + g < tl.z && yb > 0)
+            cp_async_16(at + (i * 8 + g) * 64 + t * 16, yr[i] + n0, yb);
+        const uint8_t* src =
+            reinterpret_cast<const uint8_t*>(B + (int64_t)n0 * a.r);
+        const int all = min(kCols, a.N - n0) * a.r * 2;
+#pragma unroll
+        for (int i = 0; i < MT * 2; ++i) {
+          const int p = (lane + 32 * i) * 16;
+          if (p < all)
+            cp_async_16(at + kTile * 64 + p, src + p, min(16, all - p));
+        }
+      }
+      cp_async_commit();
+    }
+  };
+  if constexpr (RING) {
+#pragma unroll
+    for (int i = 0; i < kStages<MT>; ++i) issue(part + i * parts, i);
+  } else {
+    if (part < units) fetch(part, cur);
+  }
 
   // ---- U: the warps', then the cluster's sums
   __syncthreads();
@@ -393,7 +453,27 @@ __device__ __forceinline__ void add_tile(const AddArgs<TX, TY>& a, int4 tl,
   __syncthreads();
 
   // ---- step 2
+  int slot = 0;
   for (int u = part; u < units; u += parts) {
+    const uint8_t* unit = ring + slot * kUnitBytes<MT>;
+    if constexpr (RING) {
+      cp_async_wait<kStages<MT> - 1>();
+      __syncwarp();
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int n = 8 * (g >> 1) + 2 * j + (g & 1);
+#pragma unroll
+        for (int kk = 0; kk < MT; ++kk) {
+          const int q = kk * 16 + 4 * t;
+          const uint2 v =
+              q < a.r ? *reinterpret_cast<const uint2*>(
+                            unit + kTile * 64 + (n * a.r + q) * 2)
+                      : make_uint2(0, 0);
+          cur.b[j][kk].w[0] = v.x;
+          cur.b[j][kk].w[1] = v.y;
+        }
+      }
+    }
     float c[TM][4][4] = {};
 #pragma unroll
     for (int kk = 0; kk < MT; ++kk) {
@@ -414,8 +494,25 @@ __device__ __forceinline__ void add_tile(const AddArgs<TX, TY>& a, int4 tl,
                           bt[j][x][1]);
         }
     }
+    if constexpr (RING) {
+#pragma unroll
+      for (int m = 0; m < TM; ++m)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const uint4 v = *reinterpret_cast<const uint4*>(
+              unit + (m * 16 + h * 8 + g) * 64 + t * 16);
+          cur.y[m][h].w[0] = v.x;
+          cur.y[m][h].w[1] = v.y;
+          cur.y[m][h].w[2] = v.z;
+          cur.y[m][h].w[3] = v.w;
+        }
+      __syncwarp();  // every lane has read the unit
+      issue(u + kStages<MT> * parts, slot);
+      slot = slot + 1 == kStages<MT> ? 0 : slot + 1;
+    }
     const Unit now = cur;
-    if (u + parts < units) fetch(u + parts, cur);
+    if constexpr (!RING)
+      if (u + parts < units) fetch(u + parts, cur);
     const int n = u * kCols + 8 * t;
 #pragma unroll
     for (int m = 0; m < TM; ++m)
@@ -430,7 +527,7 @@ __device__ __forceinline__ void add_tile(const AddArgs<TX, TY>& a, int4 tl,
           e[i] = from_f32<TY>(
               fmaf(c[m][i >> 1][2 * h + (i & 1)], s, to_f32(e[i])));
         TY* o = a.out + ot[m][h] + n;
-        if (a.vec && n + 8 <= a.N) {
+        if ((RING || a.vec) && n + 8 <= a.N) {
           const Raw<TY, 8>& w = *reinterpret_cast<const Raw<TY, 8>*>(e);
 #pragma unroll
           for (int i = 0; i < (int)sizeof(TY) / 2; ++i)
@@ -446,8 +543,12 @@ __device__ __forceinline__ void add_tile(const AddArgs<TX, TY>& a, int4 tl,
   }
 }
 
+// CTAs per SM: two where 128 registers hold a unit in flight.
+template <typename TX, int MT>
+constexpr int kPerSm = sizeof(TX) == 2 && MT <= 2 ? 2 : 1;
+
 template <typename TX, typename TY, int MT>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, kPerSm<TX, MT>)
     adapters_add_kernel(const AddArgs<TX, TY> a) {
   extern __shared__ __align__(16) float sm[];
   griddep_enter();
@@ -476,10 +577,20 @@ __global__ void __launch_bounds__(kThreads)
     }
     return;
   }
+  if constexpr (kRingTypes<TX, TY>) {
+    if (a.ring) {
+      if (tl.z <= 8)
+        add_tile<TX, TY, MT, 1, true>(a, tl, order, rank, ranks, sm);
+      else
+        add_tile<TX, TY, MT, 4, true>(a, tl, order, rank, ranks, sm);
+      cp_async_wait_all();
+      return;
+    }
+  }
   if (tl.z <= 8)
-    add_tile<TX, TY, MT, 1>(a, tl, order, rank, ranks, sm);
+    add_tile<TX, TY, MT, 1, false>(a, tl, order, rank, ranks, sm);
   else
-    add_tile<TX, TY, MT, 4>(a, tl, order, rank, ranks, sm);
+    add_tile<TX, TY, MT, 4, false>(a, tl, order, rank, ranks, sm);
 }
 
 }  // namespace
@@ -501,11 +612,7 @@ ttq_status launch_adapters_plan(const int32_t* index, int64_t T, int64_t L,
 ttq_status launch_adapters_add(const AdapterArgs& a, cudaStream_t st) {
   LaunchShape ls;
   const int tiles = (int)max_tiles(a.T, a.L);
-  // up to 8 CTAs share a tile: as many as fill two per SM
-  const int ranks = std::max(1, std::min(8, 2 * sm_count() / tiles));
-  ls.grid = dim3((unsigned)tiles, (unsigned)ranks);
   ls.block = dim3(kThreads);
-  ls.cluster_y = (unsigned)ranks;
   auto go = [&](auto* x, auto* y) -> ttq_status {
     using TX = std::remove_const_t<std::remove_pointer_t<decltype(x)>>;
     using TY = std::remove_pointer_t<decltype(y)>;
@@ -531,10 +638,18 @@ ttq_status launch_adapters_add(const AdapterArgs& a, cudaStream_t st) {
                          (uintptr_t)(a.ldy * sizeof(TY)) |
                          (uintptr_t)(a.ldo * sizeof(TY));
     g.vec = at % 16 == 0;
+    // every adapter's B and every unit's Y on 16-byte boundaries
+    g.ring = kRingTypes<TX, TY> && g.vec && (a.N * a.r) % 8 == 0;
     g.err = device_error_word();
     auto run = [&](auto mt) -> ttq_status {
       constexpr int MT = decltype(mt)::value;
+      // up to 8 CTAs share a tile: as many as the SMs hold at once
+      const int ranks =
+          std::max(1, std::min(8, kPerSm<TX, MT> * sm_count() / tiles));
+      ls.grid = dim3((unsigned)tiles, (unsigned)ranks);
+      ls.cluster_y = (unsigned)ranks;
       ls.smem = smem_bytes<TX, MT>();
+      if (g.ring) ls.smem += (size_t)kWarps * kStages<MT> * kUnitBytes<MT>;
       auto kern = adapters_add_kernel<TX, TY, MT>;
       if (cudaFuncSetAttribute(kern,
                                cudaFuncAttributeMaxDynamicSharedMemorySize,

@@ -30,6 +30,7 @@
 #include <cuda_fp16.h>
 
 #include <algorithm>
+#include <atomic>
 #include <type_traits>
 
 #include "common.cuh"
@@ -1192,11 +1193,19 @@ size_t down_smem(int T, int n, int E) {
          (size_t)kWarps * kRing<BITS, G16, NTMAX>;
 }
 
-template <typename K>
-bool allow_smem(K kern, size_t bytes) {
-  return cudaFuncSetAttribute(kern,
-                              cudaFuncAttributeMaxDynamicSharedMemorySize,
-                              (int)bytes) == cudaSuccess;
+// Lets a kernel use all of an SM's shared memory, once per device.
+template <auto KERN>
+bool allow_smem() {
+  static std::atomic<uint64_t> done{0};
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0) return false;
+  const uint64_t bit = (uint64_t)1 << (dev & 63);
+  if (dev < 64 && (done.load(std::memory_order_relaxed) & bit)) return true;
+  if (cudaFuncSetAttribute(KERN, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                           227 * 1024) != cudaSuccess)
+    return false;
+  if (dev < 64) done.fetch_or(bit, std::memory_order_relaxed);
+  return true;
 }
 
 inline int ctas_per_sm(size_t smem) { return smem + 1024 <= 114 * 1024 ? 2 : 1; }
@@ -1211,8 +1220,8 @@ ttq_status launch_up(UpArgs u, cudaStream_t st) {
   const int64_t tiles =
       (int64_t)Lists::max_entries(u.T * u.top_k, u.E) * (u.I / 16);
   ls.grid = dim3((unsigned)std::min<int64_t>(tiles, slots));
-  auto kern = up_kernel<BITS, G16, LG, MODE, NTMAX, LOCAL>;
-  if (!allow_smem(kern, ls.smem)) return TTQ_ERR_CUDA;
+  constexpr auto kern = up_kernel<BITS, G16, LG, MODE, NTMAX, LOCAL>;
+  if (!allow_smem<kern>()) return TTQ_ERR_CUDA;
   return launch(ls, st, kern, u);
 }
 
@@ -1232,8 +1241,8 @@ ttq_status launch_down(DownArgs d, cudaStream_t st) {
   const int ranks = std::max(1, std::min(8, slots / grid));
   ls.grid = dim3((unsigned)grid, (unsigned)ranks);
   ls.cluster_y = (unsigned)ranks;
-  auto kern = down_kernel<BITS, G16, LG, MODE, NTMAX, LOCAL>;
-  if (!allow_smem(kern, ls.smem)) return TTQ_ERR_CUDA;
+  constexpr auto kern = down_kernel<BITS, G16, LG, MODE, NTMAX, LOCAL>;
+  if (!allow_smem<kern>()) return TTQ_ERR_CUDA;
   return launch(ls, st, kern, d);
 }
 

@@ -713,12 +713,13 @@ def moe_route(X: torch.Tensor, W: torch.Tensor, top_k: int,
     if bias is not None:
         _buf(bias, "bias", torch.float32, E)
     if ids is None:
-        ids = torch.empty((T, top_k), dtype=torch.int32, device=X.device)
+        ids = X.new_empty((T, top_k), dtype=torch.int32)
+    else:
+        _buf(ids, "ids", torch.int32, T, top_k)
     if weights is None:
-        weights = torch.empty((T, top_k), dtype=torch.float32,
-                              device=X.device)
-    _buf(ids, "ids", torch.int32, T, top_k)
-    _buf(weights, "weights", torch.float32, T, top_k)
+        weights = X.new_empty((T, top_k), dtype=torch.float32)
+    else:
+        _buf(weights, "weights", torch.float32, T, top_k)
     _check(_lib.ttq_moe_route(
         X.data_ptr(), _code(X, "X"), T, K, ldx, W.data_ptr(), _code(W, "W"),
         E, ldw, _ptr(bias), int(top_k), _named(_SCORE, score, "score"),
@@ -727,6 +728,7 @@ def moe_route(X: torch.Tensor, W: torch.Tensor, top_k: int,
     return ids, weights
 
 
+@functools.lru_cache(maxsize=4096)
 def moe_lowbit_workspace_size(T: int, K: int, I: int, top_k: int) -> int:
     return int(_lib.ttq_moe_lowbit_workspace_size(T, K, I, top_k))
 
@@ -759,13 +761,15 @@ def moe_lowbit(X: torch.Tensor, ids: torch.Tensor, weights: torch.Tensor,
     _packed(*up, E * 2 * I, K, bits, group)
     _packed(*down, E * K, I, bits, group)
     if out is None:
-        out = torch.empty((T, K), dtype=out_dtype or X.dtype, device=X.device)
-    ldy = _out(out, "out", T, K)
+        out = X.new_empty((T, K), dtype=out_dtype or X.dtype)
+        ldy = K
+    else:
+        ldy = _out(out, "out", T, K)
     need = moe_lowbit_workspace_size(T, K, I, top_k)
     if workspace is None:
-        workspace = torch.empty(max(need, 16), dtype=torch.uint8,
-                                device=X.device)
-    _buf(workspace, "workspace", torch.uint8, need)
+        workspace = X.new_empty(max(need, 16), dtype=torch.uint8)
+    else:
+        _buf(workspace, "workspace", torch.uint8, need)
     _check(_lib.ttq_moe_lowbit(
         X.data_ptr(), _code(X, "X"), T, K, ldx, ids.data_ptr(),
         weights.data_ptr(), top_k, E, inv_s.data_ptr(), up[0].data_ptr(),
@@ -777,6 +781,11 @@ def moe_lowbit(X: torch.Tensor, ids: torch.Tensor, weights: torch.Tensor,
     return out
 
 
+@functools.lru_cache(maxsize=4096)
+def _plan_size(T: int, L: int) -> int:
+    return int(_lib.ttq_adapters_plan_size(T, L))
+
+
 def adapters_plan(index: torch.Tensor, L: int,
                   plan: torch.Tensor | None = None) -> torch.Tensor:
     """Groups a batch's tokens by adapter: ``index`` [T] int32 is each
@@ -784,7 +793,7 @@ def adapters_plan(index: torch.Tensor, L: int,
     adapters_add of the batch."""
     _buf(index, "index", torch.int32, 0)
     T = index.shape[0]
-    need = int(_lib.ttq_adapters_plan_size(T, int(L)))
+    need = _plan_size(T, int(L))
     if need <= 0:
         raise TTQError(f"no adapter plan for T={T}, L={L}")
     if plan is None:
@@ -815,13 +824,14 @@ def adapters_add(X: torch.Tensor, A: torch.Tensor, B: torch.Tensor,
                        f"{tuple(A.shape)} and {tuple(B.shape)}")
     if scale is not None:
         _buf(scale, "scale", torch.float32, L)
-    ldy = _out(Y, "Y", T, N)
-    out = Y if out is None else out
-    ldo = _out(out, "out", T, N)
+    ldy = ldo = _out(Y, "Y", T, N)
+    if out is None:
+        out = Y
+    else:
+        ldo = _out(out, "out", T, N)
     if out.dtype != Y.dtype:
         raise TTQError(f"out must be {Y.dtype}, got {out.dtype}")
-    need = int(_lib.ttq_adapters_plan_size(T, L))
-    _buf(plan, "plan", torch.int32, max(need, 1))
+    _buf(plan, "plan", torch.int32, max(_plan_size(T, L), 1))
     _check(_lib.ttq_adapters_add(
         X.data_ptr(), _code(X, "X"), T, K, ldx, A.data_ptr(), B.data_ptr(),
         _ptr(scale), L, r, N, plan.data_ptr(), plan.numel(), Y.data_ptr(),
