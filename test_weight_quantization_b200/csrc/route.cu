@@ -1,7 +1,7 @@
 // route.cu — the router of a mixture-of-experts layer: logits, scores and
 // each token's top_k experts (ttq_moe_route).
 //
-// One launch. A cluster of CTAs takes 8 or 16 tokens; its CTAs split K, a
+// One launch. A cluster of CTAs takes 8, 16 or 32 tokens; its CTAs split K, a
 // CTA's warps split the experts (and K further, where there are few experts).
 // The products are mma.sync m16n8k16 with 16 experts as M and 8 tokens as N,
 // every value loaded once from global memory into its fragment (a lane takes 8
@@ -12,7 +12,9 @@
 // Then a warp takes a token: scores in fp64, and top_k rounds that find the
 // largest 64-bit key by three warp reductions (high word, low word, lowest
 // expert). Bound by launch and reduction latency for few tokens; for many, by
-// reading W from L2 once per 16 tokens.
+// reading W from L2, and splitting an fp32 W into terms, once per tile of
+// tokens: 32 where 16 would not fit the SMs in one go (1000 tokens, 128
+// experts, K 4096, fp32 W: see the launch).
 #include <math.h>
 
 #include <algorithm>
@@ -276,7 +278,8 @@ ttq_status go(const void* X, int64_t T, int64_t K, int64_t ldx, const void* W,
   int ew = kWarps;
   while (ew > et) ew /= 2;
   const int mt = (et + ew - 1) / ew;  // at most 4
-  const int nt = T <= 8 ? 1 : 2;
+  // (four CTAs per tile is what K = 4096 takes)
+  const int nt = T <= 8 ? 1 : T <= (int64_t)4 * sm_count() ? 2 : 4;
   const int tiles = (int)((T + nt * 8 - 1) / (nt * 8));
   LaunchShape ls;
   // CTAs per tile: enough to fill the SMs, and parts of K of at most 1024
@@ -288,14 +291,18 @@ ttq_status go(const void* X, int64_t T, int64_t K, int64_t ldx, const void* W,
   ls.cluster_y = (unsigned)ranks;
   ls.smem = (size_t)(kWarps / ew) * nt * 8 * p.E * sizeof(float);
   auto run = [&](auto m, auto n) -> ttq_status {
-    return launch(
-        ls, st, route_kernel<TX, TW, decltype(m)::value, decltype(n)::value>,
-        static_cast<const TX*>(X), (int)T, (int)K, ldx,
-        static_cast<const TW*>(W), ldw, ew, p);
+    auto kern = route_kernel<TX, TW, decltype(m)::value, decltype(n)::value>;
+    if (ls.smem > 48 * 1024 &&
+        cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             (int)ls.smem) != cudaSuccess)
+      return TTQ_ERR_CUDA;
+    return launch(ls, st, kern, static_cast<const TX*>(X), (int)T, (int)K, ldx,
+                  static_cast<const TW*>(W), ldw, ew, p);
   };
   auto run_m = [&](auto m) -> ttq_status {
-    return nt == 1 ? run(m, std::integral_constant<int, 1>{})
-                   : run(m, std::integral_constant<int, 2>{});
+    if (nt == 1) return run(m, std::integral_constant<int, 1>{});
+    if (nt == 2) return run(m, std::integral_constant<int, 2>{});
+    return run(m, std::integral_constant<int, 4>{});
   };
   if (mt == 1) return run_m(std::integral_constant<int, 1>{});
   if (mt == 2) return run_m(std::integral_constant<int, 2>{});

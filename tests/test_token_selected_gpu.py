@@ -325,6 +325,8 @@ def route_reference(X, W, bias, score):
     (65, 100, 7, 1032, torch.float32, torch.bfloat16, "softmax", True, False),
     (300, 256, 8, 128, torch.bfloat16, torch.float16, "sigmoid", False, True),
     (16, 16, 16, 40, torch.float16, torch.bfloat16, "softmax", False, True),
+    (700, 64, 4, 1536, torch.bfloat16, torch.float32, "softmax", False, True),
+    (601, 512, 3, 136, torch.float16, torch.float16, "sigmoid", True, True),
 ])
 def test_route(ttq, T, E, k, K, dt, wt, score, bias, renorm):
     g = gen("route", T, E, k, K, score)
