@@ -885,16 +885,156 @@ class TTQLinear:
         quantize_rtn_grouped(self.W, self.s, p.bits, p.group, self.codes,
                              self.delta, self.zero)
 
-    def project(self, X: torch.Tensor, out: torch.Tensor | None = None):
+    def project(self, X: torch.Tensor, out: torch.Tensor | None = None,
+                adapters: "tuple[AdapterBank, torch.Tensor] | None" = None):
+        """The projection of X; with ``adapters`` (a bank and the batch's
+        plan) each token's adapter is added to it."""
         T, K = X.shape
         r = 0 if self.A is None else self.A.shape[0]
         need = workspace_size(T, K, r)
         if self._ws is None or self._ws.numel() < need:
             self._ws = torch.empty(need, dtype=torch.uint8, device=X.device)
-        return w_lowbit_gemm(X, self.inv_s, self.codes, self.delta, self.zero,
-                             self.W.shape[0], self.prm.bits, self.prm.group,
-                             self.A, self.B, out=out, workspace=self._ws)
+        Y = w_lowbit_gemm(X, self.inv_s, self.codes, self.delta, self.zero,
+                          self.W.shape[0], self.prm.bits, self.prm.group,
+                          self.A, self.B, out=out, workspace=self._ws)
+        if adapters is not None:
+            bank, plan = adapters
+            bank.add(X, plan, Y)
+        return Y
 
-    def __call__(self, X: torch.Tensor, out: torch.Tensor | None = None):
+    def __call__(self, X: torch.Tensor, out: torch.Tensor | None = None,
+                 adapters: "tuple[AdapterBank, torch.Tensor] | None" = None):
         self.calibrate(X)
-        return self.project(X, out)
+        return self.project(X, out, adapters)
+
+
+class AdapterBank:
+    """The low-rank adapters of one layer: A [L, r, K], B [L, N, r] (an
+    adapter of a lower rank padded with zeros) and scale [L] fp32. One plan
+    per batch serves the banks of all layers with L adapters."""
+
+    def __init__(self, A: torch.Tensor, B: torch.Tensor,
+                 scale: torch.Tensor | None = None):
+        self.A, self.B, self.scale = A, B, scale
+
+    def plan(self, index: torch.Tensor) -> torch.Tensor:
+        """The batch's plan from each token's adapter (negative: none)."""
+        return adapters_plan(index, self.A.shape[0])
+
+    def add(self, X: torch.Tensor, plan: torch.Tensor, Y: torch.Tensor,
+            out: torch.Tensor | None = None) -> torch.Tensor:
+        return adapters_add(X, self.A, self.B, plan, Y, self.scale, out)
+
+
+class TTQMoE:
+    """A mixture-of-experts layer run the TTQ way.
+
+    ``prompt(X)``: statistics and scales of the layer's input, shared by all
+    experts, and every expert's gate and up weights quantized by them; then,
+    expert by expert, its tokens' projection, the statistics and scales of
+    its own intermediate activations, and its down weight quantized by those.
+    An expert that meets no token of the prompt keeps scales of 1 for its
+    down weight. ``decode(X)`` runs up to 64 tokens on the packed experts:
+    the router and the whole layer, without a copy to the host.
+
+    ``router`` [E, K], ``W_up`` [E, 2I, K] (gate rows first), ``W_down``
+    [E, K, I]. One object serves one stream at a time.
+    """
+
+    def __init__(self, router: torch.Tensor, W_up: torch.Tensor,
+                 W_down: torch.Tensor, params: TTQParams, top_k: int,
+                 act: str = "silu", score: str = "softmax",
+                 bias: torch.Tensor | None = None, renormalize: bool = True,
+                 scaling: float = 1.0):
+        E, K, I = W_down.shape
+        if tuple(W_up.shape) != (E, 2 * I, K) or \
+                tuple(router.shape) != (E, K):
+            raise TTQError(f"router must be [E, K] and W_up [E, 2I, K] for "
+                           f"W_down {tuple(W_down.shape)}, got "
+                           f"{tuple(router.shape)} and {tuple(W_up.shape)}")
+        _named(_ACT, act, "act")
+        _named(_SCORE, score, "score")
+        self.router, self.W_up, self.W_down = router, W_up, W_down
+        self.prm, self.top_k, self.act = params, top_k, act
+        self.route_args = dict(bias=bias, score=score,
+                               renormalize=renormalize, scaling=scaling)
+        f32 = dict(dtype=torch.float32, device=W_up.device)
+        self.sums = torch.empty(K, **f32)
+        self.s, self.inv_s = torch.empty(K, **f32), torch.empty(K, **f32)
+        self.sums_mid = torch.empty(I, **f32)
+        self.s_mid = torch.ones(E, I, **f32)
+        self.inv_s_mid = torch.ones(E, I, **f32)
+        self.counter = new_counter(W_up.device)
+        self.up = self._packed_buffers(E * 2 * I, K)
+        self.down = self._packed_buffers(E * K, I)
+        self._ws = None
+
+    def _packed_buffers(self, N: int, K: int):
+        dev, gl = self.W_up.device, groups_ld(K, self.prm.group)
+        return (torch.empty((N, codes_ld(K, self.prm.bits)),
+                            dtype=torch.int32, device=dev),
+                torch.empty((N, gl), dtype=torch.float32, device=dev),
+                torch.empty((N, gl), dtype=torch.uint8, device=dev))
+
+    def route(self, X: torch.Tensor):
+        """(ids, weights) of the tokens' experts."""
+        return moe_route(X, self.router, self.top_k, **self.route_args)
+
+    def prompt(self, X: torch.Tensor) -> torch.Tensor:
+        """Quantizes the experts for this prompt and runs it, [T, K]."""
+        p = self.prm
+        E, K, I = self.W_down.shape
+        act_stats_scales(X, self.counter, p.alpha, p.lam, p.p, self.sums,
+                         self.s, self.inv_s)
+        quantize_rtn_grouped(self.W_up.view(E * 2 * I, K), self.s, p.bits,
+                             p.group, *self.up)
+        ids, weights = self.route(X)
+        # the experts' tokens: one read of the choices by the host
+        order = torch.argsort(ids.view(-1), stable=True)
+        counts = torch.bincount(ids.view(-1).long(), minlength=E).tolist()
+        Y = torch.zeros(X.shape, dtype=torch.float32, device=X.device)
+        self.s_mid.fill_(1.0)
+        self.inv_s_mid.fill_(1.0)
+        f = torch.nn.functional
+        at = 0
+        for e, n in enumerate(counts):
+            slots = order[at:at + n]
+            at += n
+            down = tuple(b[e * K:(e + 1) * K] for b in self.down)
+            h = None
+            if n:
+                t = slots // self.top_k
+                up = tuple(b[e * 2 * I:(e + 1) * 2 * I] for b in self.up)
+                gu = w_lowbit_gemm(X[t], self.inv_s, *up, 2 * I, p.bits,
+                                   p.group, out_dtype=torch.float32)
+                g = f.silu(gu[:, :I]) if self.act == "silu" else \
+                    f.gelu(gu[:, :I], approximate="tanh")
+                h = (g * gu[:, I:]).to(X.dtype)
+                act_stats_scales(h, self.counter, p.alpha, p.lam, p.p,
+                                 self.sums_mid, self.s_mid[e],
+                                 self.inv_s_mid[e])
+            quantize_rtn_grouped(self.W_down[e], self.s_mid[e], p.bits,
+                                 p.group, *down)
+            if n:
+                y = w_lowbit_gemm(h, self.inv_s_mid[e], *down, K, p.bits,
+                                  p.group, out_dtype=torch.float32)
+                Y.index_add_(0, t, y * weights.view(-1)[slots][:, None])
+        return Y.to(X.dtype)
+
+    def decode(self, X: torch.Tensor,
+               out: torch.Tensor | None = None) -> torch.Tensor:
+        """Up to 64 tokens on the experts the last prompt quantized."""
+        T, K = X.shape
+        ids, weights = self.route(X)
+        need = moe_lowbit_workspace_size(T, K, self.inv_s_mid.shape[1],
+                                         self.top_k)
+        if self._ws is None or self._ws.numel() < need:
+            self._ws = torch.empty(max(need, 16), dtype=torch.uint8,
+                                   device=X.device)
+        return moe_lowbit(X, ids, weights, self.inv_s, self.up,
+                          self.inv_s_mid, self.down, self.prm.bits,
+                          self.prm.group, act=self.act, out=out,
+                          workspace=self._ws)
+
+    def __call__(self, X: torch.Tensor) -> torch.Tensor:
+        return self.prompt(X)

@@ -572,7 +572,8 @@ def test_adapters_a_bad_token_stays_alone(ttq):
 
 
 def test_adapters_results_do_not_depend_on_the_batch(ttq):
-    """A token's result is the same bits alone and in any batch."""
+    """A token's result is the same bits in a batch of another order and
+    size (where as many CTAs share a tile)."""
     a = make_adapters(90, 3, 16, 256, 192, torch.bfloat16)
     all_out = check_adapters(ttq, a)
     pick = torch.tensor([0, 17, 44, 89])
@@ -600,3 +601,110 @@ def test_adapters_captured_and_replayed(ttq):
         graph.replay()
         torch.cuda.synchronize()
         assert torch.equal(out, check_adapters(ttq, b))
+
+
+# ------------------------------------------------------------------ together
+
+def make_layer(ttq, E, k, K, I, act="silu", dt=torch.bfloat16, score="softmax"):
+    g = gen("layer", E, K, I)
+    router = (torch.randn(E, K, generator=g) / math.sqrt(K)).to(dt).cuda()
+    W1 = (torch.randn(E, 2 * I, K, generator=g) / math.sqrt(K)).to(dt).cuda()
+    W2 = (torch.randn(E, K, I, generator=g) / math.sqrt(I)).to(dt).cuda()
+    return ttq.TTQMoE(router, W1, W2, ttq.TTQParams(4, 32), k, act=act,
+                      score=score)
+
+
+@pytest.mark.parametrize("act,score", [("silu", "softmax"),
+                                       ("gelu", "sigmoid")])
+def test_moe_layer_prompt_then_decode(ttq, act, score):
+    layer = make_layer(ttq, 6, 2, 256, 128, act, torch.float32, score)
+    X = torch.randn(40, 256, generator=gen("px")).cuda()
+    Y = layer.prompt(X)
+    # the same tokens by the decode form, against its own bound
+    ids, w = layer.route(X)
+    m = dict(X=X, ids=ids, weights=w, inv_s=layer.inv_s, up=layer.up,
+             inv_s_mid=layer.inv_s_mid, down=layer.down, bits=4, group=32)
+    D = check_moe(ttq, m, act)
+    assert torch.equal(layer.decode(X), D)
+    # and the prompt's pass within the projection's tolerance (2e-3 each),
+    # twice through h (both factors), once through the down projection
+    fro = ((Y - D).norm() / D.norm()).item()
+    assert fro <= 3 * 2e-3, fro
+    # the scales are the framework's own statistics of this prompt
+    s, inv = ttq.awq_scales(ttq.act_stats(X), 40)
+    assert torch.allclose(layer.inv_s, inv, rtol=1e-5)
+    # an expert that no token picked keeps scales of 1
+    one = make_layer(ttq, 6, 1, 256, 128)
+    one.prompt(X[:1].bfloat16())
+    hit = int(one.route(X[:1].bfloat16())[0][0, 0])
+    rest = [e for e in range(6) if e != hit]
+    assert (one.inv_s_mid[rest] == 1).all()
+    assert not (one.inv_s_mid[hit] == 1).all()
+
+
+def test_linear_with_adapters(ttq):
+    T, K, N, L = 37, 256, 320, 5
+    g = gen("lin")
+    W = (torch.randn(N, K, generator=g) / math.sqrt(K)).bfloat16().cuda()
+    a = make_adapters(T, L, 16, K, N, torch.bfloat16)
+    lin = ttq.TTQLinear(W, ttq.TTQParams(4, 32))
+    bank = ttq.AdapterBank(a["A"], a["B"], a["scale"])
+    plan = bank.plan(a["index"])
+    base = lin(a["X"])
+    got = lin.project(a["X"], adapters=(bank, plan))
+    a["Y"] = base
+    ref, bound, live = adapters_reference(a, a["scale"])
+    assert ((got.double().cpu() - ref).abs() <= bound)[live].all()
+    assert torch.equal(got[~live.cuda()], base[~live.cuda()])
+    assert torch.equal(lin(a["X"], adapters=(bank, plan)), got)
+
+
+def test_a_decode_step_of_all_of_them_captured(ttq):
+    """A projection with its requests' adapters, then the expert layer, as one
+    graph: replayed on new tokens and adapters it gives the eager bits."""
+    T, K, L = 12, 256, 7
+    layer = make_layer(ttq, 8, 2, K, 128)
+    layer.prompt(torch.randn(90, K, generator=gen("p")).bfloat16().cuda())
+    W = (torch.randn(K, K, generator=gen("w")) / 16).bfloat16().cuda()
+    lin = ttq.TTQLinear(W, ttq.TTQParams(4, 32))
+    lin.calibrate(torch.randn(90, K, generator=gen("q")).bfloat16().cuda())
+    a = make_adapters(T, L, 8, K, K, torch.bfloat16)
+    bank = ttq.AdapterBank(a["A"], a["B"], a["scale"])
+
+    def step(X, index):
+        Y = lin.project(X, adapters=(bank, bank.plan(index)))
+        return layer.decode(Y)
+    X, index = a["X"].clone(), a["index"].clone()
+    step(X, index)  # workspaces exist before the capture
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = step(X, index)
+    for seed in range(3):
+        b = make_adapters(T, L, 8, K, K, torch.bfloat16, seed=seed)
+        want = step(b["X"], b["index"])
+        X.copy_(b["X"])
+        index.copy_(b["index"])
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, want)
+    assert ttq.device_error() == 0
+
+
+def test_calls_on_a_side_stream_follow_its_work(ttq):
+    """Inputs written on the same side stream just before the calls."""
+    m = make_moe(ttq, 1, 8, 4, 512, 256, 4, 64, torch.bfloat16)
+    want = check_moe(ttq, m)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        for _ in range(20):
+            up = tuple(torch.zeros_like(p) for p in m["up"])
+            X, ids = torch.zeros_like(m["X"]), torch.zeros_like(m["ids"])
+            w = torch.zeros_like(m["weights"])
+            for d, s in zip(up + (X, ids, w),
+                            m["up"] + (m["X"], m["ids"], m["weights"])):
+                d.copy_(s)
+            got = ttq.moe_lowbit(X, ids, w, m["inv_s"], up, m["inv_s_mid"],
+                                 m["down"], 4, 64)
+            assert torch.equal(got, want)
