@@ -545,13 +545,18 @@ __device__ __forceinline__ void subtract(uint32_t& p, __half2 z) {
 // instructions apart), otherwise nblocks. xp[n] (and xp[n] + term for the
 // second term) points at the lane's activations of the stage: 16 bytes per
 // 32-channel block, 64 bytes apart, .x and .y for the block's first MMA, .z
-// and .w for its second; xv holds the first block's.
-template <int BITS, bool G16, int LG, bool FULL, int MODE, int NT, int NTMAX>
+// and .w for its second. x holds those of the next DEPTH blocks and is refilled
+// as it is used, across stages, while there are blocks (`more` from the
+// stage's first on): they come from L1 or L2, further away than a block of
+// instructions.
+template <int BITS, bool G16, int LG, bool FULL, int MODE, int NT, int NTMAX,
+          int DEPTH>
 __device__ __forceinline__ void stage_products(
     const uint8_t* st, const uint8_t* dd, int j0,
     const Field<BITS, G16, MODE == kExact>& f, int nblocks,
     const uint4* const (&xp)[NTMAX], int64_t term,
-    uint4 (&xv)[NTMAX][kTerms<MODE>], float (&acc)[2][NTMAX][4], int lane) {
+    int more, uint4 (&x)[DEPTH][NT][kTerms<MODE>],
+    float (&acc)[2][NTMAX][4], int lane) {
   constexpr int TERMS = kTerms<MODE>;
   constexpr bool kCentre = MODE == kExact;
   constexpr int kD = kPieceDelta<G16>;
@@ -607,17 +612,7 @@ __device__ __forceinline__ void stage_products(
 #pragma unroll
   for (int b = 0; b < 4; ++b) {
     if (FULL || b < nblocks) {
-      // the next block's activations, where they fit the registers
-      constexpr bool kAhead = NT * TERMS <= 2;
-      uint4 xn[NT][TERMS];
-#pragma unroll
-      for (int n = 0; n < NT; ++n)
-#pragma unroll
-        for (int k = 0; k < TERMS; ++k) {
-          if (kAhead && b < 3 && (FULL || b + 1 < nblocks))
-            xn[n][k] = xp[n][k * term + (b + 1) * 4];
-          if (!kAhead && b > 0) xv[n][k] = xp[n][k * term + b * 4];
-        }
+      uint4(&xv)[NT][TERMS] = x[b % DEPTH];
       uint32_t p[2][2][4];  // [row tile][row g, row g + 8][pair]
       if (!G16 && (b & ((1 << LG) - 1)) == 0) centre(b >> LG);
 #pragma unroll
@@ -661,11 +656,13 @@ __device__ __forceinline__ void stage_products(
                        h == 0 && k == 0 && (b & ((1 << LG) - 1)) == 0);
         if (((b + 1) & ((1 << LG) - 1)) == 0) flush(b >> LG);
       }
+      if (b + DEPTH < more) {
 #pragma unroll
-      for (int n = 0; n < NT; ++n)
+        for (int n = 0; n < NT; ++n)
 #pragma unroll
-        for (int k = 0; k < TERMS; ++k)
-          if (kAhead && b < 3) xv[n][k] = xn[n][k];
+          for (int k = 0; k < TERMS; ++k)
+            xv[n][k] = xp[n][k * term + (b + DEPTH) * 4];
+      }
     }
   }
 }
@@ -793,12 +790,19 @@ struct Tile {
     constexpr int kPer = G16 ? 8 : 4 >> LG;  // groups per chunk
     const int lo = c * kPer;
     const int hi = min(c_end * kPer, G16 ? m.blocks * 2 : m.blocks >> LG);
-    for (; c < c_end; ++c) {
-      uint4 xv[NTMAX][TERMS];
+    // blocks of activations in flight: what the registers hold
+    constexpr int DEPTH = NT * TERMS <= 2 ? 2 : 1;
+    const int last = min(c_end * 4, m.blocks);
+    uint4 x[DEPTH][NT][TERMS];
+#pragma unroll
+    for (int d = 0; d < DEPTH; ++d)
 #pragma unroll
       for (int n = 0; n < NT; ++n)
 #pragma unroll
-        for (int k = 0; k < TERMS; ++k) xv[n][k] = xp[n][k * term];
+        for (int k = 0; k < TERMS; ++k)
+          x[d][n][k] = 4 * c + d < last ? xp[n][k * term + d * 4]
+                                        : make_uint4(0, 0, 0, 0);
+    for (; c < c_end; ++c) {
       cp_async_wait<S - 1>();
       __syncwarp();  // every lane's part of the stage is there
       if (fresh || m.new_piece(c)) {
@@ -814,11 +818,11 @@ struct Tile {
       const int j0 = G16 ? 0 : (c * (4 >> LG)) & 3;
       const int nb = m.blocks - 4 * c;
       if (nb >= 4)
-        stage_products<BITS, G16, LG, true, MODE, NT, NTMAX>(
-            st, dd, j0, f, 4, xp, term, xv, acc, lane);
+        stage_products<BITS, G16, LG, true, MODE, NT, NTMAX, DEPTH>(
+            st, dd, j0, f, 4, xp, term, last - 4 * c, x, acc, lane);
       else
-        stage_products<BITS, G16, LG, false, MODE, NT, NTMAX>(
-            st, dd, j0, f, nb, xp, term, xv, acc, lane);
+        stage_products<BITS, G16, LG, false, MODE, NT, NTMAX, DEPTH>(
+            st, dd, j0, f, nb, xp, term, last - 4 * c, x, acc, lane);
 #pragma unroll
       for (int n = 0; n < NT; ++n) xp[n] += 16;
       stage = stage + 1 == S ? 0 : stage + 1;
