@@ -59,12 +59,11 @@ template <bool G16>
 constexpr int kPiece = kRows * (kPieceDelta<G16> + kPieceDelta<G16> / 4);
 // Stages per warp: what lets two CTAs of 8 warps share an SM. As many pieces:
 // a stage needs at most one new one.
-#ifndef TTQ_S2
-#define TTQ_S2 2
-#endif
+// Two are enough beside 16 columns (three: 131 against 120 us for 16 tokens,
+// 32 experts of 2560 x 1728 at 3 bits), and leave the rest to L1.
 template <int BITS, int NTMAX>
-constexpr int kStages = NTMAX == 1 ? (BITS <= 3 ? 5 : BITS <= 5 ? 3 : 2)
-                                   : (BITS <= 3 ? TTQ_S2 + 1 : BITS <= 5 ? TTQ_S2 : 2);
+constexpr int kStages = BITS <= 3 ? (NTMAX == 1 ? 5 : 3)
+                        : BITS <= 5 && NTMAX == 1 ? 3 : 2;
 template <int BITS, bool G16, int NTMAX>
 constexpr int kRing = kStages<BITS, NTMAX> * (kStage<BITS> + kPiece<G16>);
 // Where the rows a CTA converts itself start: after the rings, which start at
@@ -866,8 +865,11 @@ __global__ void __launch_bounds__(kThreads, 2)
                         warp * kRing<BITS, G16, NTMAX>;
   const uint32_t ring_at = smem_u32(ring);
 
-  // ids and the packed weights were complete before the kernel that runs
-  // before this one started: lists and the first stages need not wait for it
+  // Behind rows_kernel, ids and the packed weights were complete before that
+  // kernel let this one start: lists and the first stages need not wait for
+  // it. With LOCAL this is the call's first kernel, and whatever runs before it
+  // (the router, the quantizer) may still be writing them.
+  if constexpr (LOCAL) griddep_enter();
   build_lists(l, a.ids, nullptr, a.T, a.top_k, a.E, a.err);
   const int tiles = a.I / 16;  // of an entry
   const int chunks = (a.K + kChunk - 1) / kChunk;
@@ -921,7 +923,7 @@ __global__ void __launch_bounds__(kThreads, 2)
   };
 #pragma unroll
   for (int i = 0; i < S; ++i) issue();
-  griddep_enter();
+  if constexpr (!LOCAL) griddep_enter();
 
   const uint4* xhat = a.xhat;
   const float* xsum = a.xsum;
@@ -1059,8 +1061,8 @@ __global__ void __launch_bounds__(kThreads, 2)
   const uint32_t ring_at = smem_u32(ring);
   float* mine = ysum + warp * region;
 
-  // as in up_kernel: nothing before griddep_enter() reads what the kernel
-  // before this one writes
+  // nothing before griddep_enter() reads what the kernel before this one
+  // writes, and that kernel let this one start only after its own wait
   build_lists(l, a.ids, a.weights, a.T, a.top_k, a.E, nullptr);
   for (int i = lane; i < region; i += 32) mine[i] = 0.f;
   const int rs = a.rs, ks = kWarps / rs;

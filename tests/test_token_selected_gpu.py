@@ -178,6 +178,8 @@ def test_moe_types(ttq, dt, out_dt, act):
     (64, 40, 32, 64, 64, 6, 64),     # the most choices
     (16, 16, 2, 4096, 64, 4, 64),    # wide in, narrow middle
     (16, 16, 2, 64, 4096, 4, 64),    # narrow out, wide middle
+    (16, 64, 8, 64, 1024, 4, 32),    # whole rounds of tiles per CTA
+    (12, 64, 8, 160, 1024, 3, 16),   # and a rest, chunks that end early
 ])
 def test_moe_sizes(ttq, T, E, k, K, I, bits, group):
     check_moe(ttq, make_moe(ttq, T, E, k, K, I, bits, group, torch.bfloat16))
@@ -708,3 +710,33 @@ def test_calls_on_a_side_stream_follow_its_work(ttq):
             got = ttq.moe_lowbit(X, ids, w, m["inv_s"], up, m["inv_s_mid"],
                                  m["down"], 4, 64)
             assert torch.equal(got, want)
+
+
+def test_one_token_right_behind_its_router_and_quantizer(ttq):
+    """The layer's first kernel may start while the kernel before it still
+    runs: it must not read that kernel's ids or codes early."""
+    g = gen("behind")
+    E, K, I, k = 256, 512, 128, 4
+    layer = make_layer(ttq, E, k, K, I)
+    layer.prompt(torch.randn(300, K, generator=g).bfloat16().cuda())
+    xs = [torch.randn(1, K, generator=g).bfloat16().cuda() for _ in range(40)]
+    want = []
+    for x in xs:
+        ids, w = layer.route(x)
+        torch.cuda.synchronize()
+        want.append(ttq.moe_lowbit(x, ids, w, layer.inv_s, layer.up,
+                                   layer.inv_s_mid, layer.down, 4, 32))
+        torch.cuda.synchronize()
+    got = [layer.decode(x) for x in xs]
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+    # the up weights quantized anew just before the call
+    W = layer.W_up.view(E * 2 * I, K)
+    ids, w = layer.route(xs[0])
+    for _ in range(20):
+        for b in layer.up:
+            b.zero_()
+        ttq.quantize_rtn_grouped(W, layer.s, 4, 32, *layer.up)
+        out = ttq.moe_lowbit(xs[0], ids, w, layer.inv_s, layer.up,
+                             layer.inv_s_mid, layer.down, 4, 32)
+        assert torch.equal(out, want[0])
