@@ -476,7 +476,9 @@ ttq_status ttq_moe_route(const void* X, ttq_dtype xt, int64_t T, int64_t K,
  *   workspace  ttq_moe_lowbit_workspace_size(T, K, I, top_k) bytes,
  *            16-byte aligned, caller-owned; scratch, overwritten. Calls that
  *            may overlap on the GPU need different workspaces.
- * Codes are multiplied as exact integers and Delta is applied in fp32. The
+ * Codes are multiplied as exact integers and Delta is applied in fp32; the
+ * zero points' share, Delta zero times the group's sum of activations, in two
+ * tf32 terms of each factor (22 bits; fp32 Y: the exact code less zero). The
  * activations x and h inv_s_mid are scaled by a power of two per token and
  * rounded once to fp16 for a bf16 Y, or held in two fp16 terms (22 bits) for
  * an fp16 or fp32 Y; sums are fp32. Every expert's weights are read once

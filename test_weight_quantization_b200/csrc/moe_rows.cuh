@@ -83,6 +83,10 @@ __device__ __forceinline__ void store_vector(const RowFormat& f, int i,
   fac[1] = g16 ? (second ? s3 : s1) : s1;
   fac[2] = g16 ? fac[0] : s2;
   fac[3] = g16 ? fac[1] : s3;
+  float inv[4];  // of powers of two
+#pragma unroll
+  for (int q = 0; q < 4; ++q)
+    inv[q] = __uint_as_float(0x7F000000u - __float_as_uint(fac[q]));
 #pragma unroll
   for (int q = 0; q < 8; ++q) v[q] = v[q] * sc * fac[q & 3];
   float total = 0.f;
@@ -115,7 +119,7 @@ __device__ __forceinline__ void store_vector(const RowFormat& f, int i,
     }
 #pragma unroll
     for (int q = 0; q < 8; ++q) {
-      total += a[q] / fac[q & 3];
+      total += a[q] * inv[q & 3];
       v[q] -= a[q];
     }
   }
@@ -125,12 +129,14 @@ __device__ __forceinline__ void store_vector(const RowFormat& f, int i,
   if (live && i % lanes == 0) sums[i / lanes] = total;
 }
 
-// rows rows (row j read at src(j)) to shared memory, by the whole CTA. mx:
-// shared, a word per row. Ends with a __syncthreads().
+// rows rows (row j read at src(j)) to shared memory, by the whole CTA; `term`
+// vectors between the terms. mx: shared, a word per row. Ends with a
+// __syncthreads().
 template <int THREADS, typename SF>
 __device__ __forceinline__ void convert_rows(const RowFormat& f, int rows,
                                              int n, const float* inv_s,
-                                             uint4* out, float* sums, int ldg,
+                                             uint4* out, int term,
+                                             float* sums, int ldg,
                                              uint32_t* mx, SF&& src) {
   const int tid = threadIdx.x, all = rows * n;
   if (tid < rows) mx[tid] = 0;
@@ -148,7 +154,7 @@ __device__ __forceinline__ void convert_rows(const RowFormat& f, int rows,
     const int r = live ? i / n : 0, j = live ? i - r * n : 0;
     float v[8] = {};
     if (live) load_scaled(src(r), inv_s, j, v);
-    store_vector(f, j, mx[r], live, v, out + r * n, all, sums + r * ldg);
+    store_vector(f, j, mx[r], live, v, out + r * n, term, sums + r * ldg);
   }
   __syncthreads();
 }

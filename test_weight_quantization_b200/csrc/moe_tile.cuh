@@ -936,8 +936,9 @@ __global__ void __launch_bounds__(kThreads, 2)
         x + (int64_t)a.T * a.K / 8 * a.format.terms);
     uint32_t* mx = reinterpret_cast<uint32_t*>(sum + a.T * m.ldg);
     auto convert = [&](auto* rows) {
-      convert_rows<kThreads>(a.format, a.T, a.K / 8, a.inv_s, x, sum, m.ldg,
-                             mx, [&](int r) { return rows + r * a.ldx; });
+      convert_rows<kThreads>(a.format, a.T, a.K / 8, a.inv_s, x,
+                             a.T * (a.K / 8), sum, m.ldg, mx,
+                             [&](int r) { return rows + r * a.ldx; });
     };
     if (a.xt == TTQ_F32)
       convert(static_cast<const float*>(a.X));
@@ -1069,7 +1070,8 @@ __global__ void __launch_bounds__(kThreads, 2)
   const int wr = warp % rs, wk = warp / rs;
   const int tile = blockIdx.x * rs + wr;
   const int chunks = (a.I + kChunk - 1) / kChunk;
-  const int total = tile * kRows < a.K ? l.entries * chunks : 0;
+  const int whole = l.entries * chunks;
+  const int total = tile * kRows < a.K ? whole : 0;
   const int ranks = gridDim.y, rank = blockIdx.y;
   const int parts = ranks * ks, part = rank * ks + wk;
   const int s0 = (int)((unsigned)total * part / parts);
@@ -1100,6 +1102,7 @@ __global__ void __launch_bounds__(kThreads, 2)
   const float* hsum = a.hsum;
   const uint32_t* hmax = a.hmax;
   const int slots = a.T * a.top_k;
+  int row0 = 0;  // LOCAL: rows are columns from here on, otherwise slots
   if constexpr (LOCAL) {
     uint4* x = reinterpret_cast<uint4*>(sm + smem_rows<BITS, G16, NTMAX>(
         (int)(reinterpret_cast<const uint8_t*>(ysum) - sm) +
@@ -1107,9 +1110,17 @@ __global__ void __launch_bounds__(kThreads, 2)
     float* sum =
         reinterpret_cast<float*>(x + (int64_t)slots * a.I / 8 * a.format.terms);
     uint32_t* mx = reinterpret_cast<uint32_t*>(sum + slots * m.ldg);
-    // (the row of a choice without an expert is whatever h holds: not used)
-    convert_rows<kThreads>(a.format, slots, a.I / 8, nullptr, x, sum, m.ldg,
-                           mx, [&](int r) { return a.h + (int64_t)r * a.I; });
+    // the columns of the entries that the CTA's parts meet
+    const int from = (int)((unsigned)whole * (rank * ks) / parts);
+    const int to = (int)((unsigned)whole * (rank * ks + ks) / parts);
+    if (from < to) {
+      const int e0 = from / chunks, e1 = (to - 1) / chunks;
+      row0 = l.first[e0];
+      convert_rows<kThreads>(
+          a.format, l.first[e1] + l.cols[e1] - row0, a.I / 8, nullptr, x,
+          slots * (a.I / 8), sum, m.ldg, mx,
+          [&](int r) { return a.h + (int64_t)l.slot[row0 + r] * a.I; });
+    }
     hhat = x;
     hsum = sum;
     hmax = mx;
@@ -1120,7 +1131,10 @@ __global__ void __launch_bounds__(kThreads, 2)
   while (s < s1) {
     const int cols = l.cols[en], col0 = l.first[en];
     tl.start(m, hhat, hsum, cols, c,
-             [&](int col) { return (int64_t)l.slot[col0 + col]; });
+             [&](int col) {
+               return (int64_t)(LOCAL ? col0 + col - row0
+                                      : l.slot[col0 + col]);
+             });
     const int stop = min(s1, s + chunks - c);
     tl.template run<LG>(m, c, c + stop - s, issue);
     s = stop;
@@ -1134,9 +1148,9 @@ __global__ void __launch_bounds__(kThreads, 2)
       for (int i = 0; i < 2; ++i) {
         const int col = n * 8 + 2 * t + i;
         if (col < cols) {
-          const int slot = l.slot[col0 + col];
+          const int r = LOCAL ? col0 + col - row0 : l.slot[col0 + col];
           const float wt =
-              l.weight[col0 + col] * row_unscale(hmax[slot], most) *
+              l.weight[col0 + col] * row_unscale(hmax[r], most) *
               per_unit;
           float* y = mine + l.token[col0 + col] * kRows + g;
           y[0] = fmaf(wt, tl.acc[0][n][i], y[0]);
