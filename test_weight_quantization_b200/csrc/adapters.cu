@@ -232,7 +232,8 @@ __device__ __forceinline__ void add_tile(const AddArgs<TX, TY>& a, int4 tl,
   const int blocks = (a.K + 31) / 32;
   const int b0 = (int)((int64_t)blocks * part / parts);
   const int b1 = (int)((int64_t)blocks * (part + 1) / parts);
-  constexpr int UN = MT * 2 + NT <= 6 && XT == 1 ? 4 : 2;  // blocks in flight
+  // blocks in flight
+  constexpr int UN = XT > 1 && MT == 4 ? 1 : MT * 2 + NT <= 6 && XT == 1 ? 4 : 2;
   for (int bb = b0; bb < b1; bb += UN) {
     Raw<TX, 8> ra[UN][MT][2], rx[UN][NT];
 #pragma unroll
@@ -259,17 +260,28 @@ __device__ __forceinline__ void add_tile(const AddArgs<TX, TY>& a, int4 tl,
         uint32_t at[2][XT][4];
         terms<TX, TX, 8>(ra[u][m][0], at[0]);
         terms<TX, TX, 8>(ra[u][m][1], at[1]);
+        // The tensor core cuts its sums instead of rounding them. Over a long
+        // K that adds up to more than fp32 values should lose (K = 10^4: 1.5e-6
+        // against 5e-7), so their blocks are summed apart and added rounded.
+        float sum[NT][4] = {};
+        float(&to)[NT][4] = XT > 1 ? sum : acc[m];
 #pragma unroll
         for (int h = 0; h < 2; ++h)
 #pragma unroll
           for (int n = 0; n < NT; ++n)
 #pragma unroll
-            for (int i = 0; i < XT; ++i)
+            for (int i = XT - 1; i >= 0; --i)
 #pragma unroll
-              for (int j = 0; j + i < XT; ++j)
-                mma<HALF>(acc[m][n], at[0][i][2 * h], at[1][i][2 * h],
+              for (int j = XT - 1 - i; j >= 0; --j)
+                mma<HALF>(to[n], at[0][i][2 * h], at[1][i][2 * h],
                           at[0][i][2 * h + 1], at[1][i][2 * h + 1],
                           xt[n][j][2 * h], xt[n][j][2 * h + 1]);
+        if constexpr (XT > 1) {
+#pragma unroll
+          for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) acc[m][n][i] += sum[n][i];
+        }
       }
     }
   }

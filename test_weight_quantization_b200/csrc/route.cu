@@ -206,18 +206,25 @@ __global__ void __launch_bounds__(kThreads)
         uint32_t wt[2][WT][4];
         terms<TW, TX, 8>(rw[u][m][0], wt[0]);
         terms<TW, TX, 8>(rw[u][m][1], wt[1]);
+        // the tensor core cuts its sums instead of rounding them: a block is
+        // summed apart and added rounded
+        float sum[NT][4] = {};
 #pragma unroll
         for (int h = 0; h < 2; ++h)
 #pragma unroll
           for (int n = 0; n < NT; ++n)
 #pragma unroll
-            for (int i = 0; i < WT; ++i)
+            for (int i = WT - 1; i >= 0; --i)
 #pragma unroll
-              for (int j = 0; j < XT; ++j)
+              for (int j = XT - 1; j >= 0; --j)
                 if (i + j <= 2)
-                  mma<HALF>(acc[m][n], wt[0][i][2 * h], wt[1][i][2 * h],
+                  mma<HALF>(sum[n], wt[0][i][2 * h], wt[1][i][2 * h],
                             wt[0][i][2 * h + 1], wt[1][i][2 * h + 1],
                             xt[n][j][2 * h], xt[n][j][2 * h + 1]);
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) acc[m][n][i] += sum[n][i];
       }
     }
   }

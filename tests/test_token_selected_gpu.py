@@ -740,3 +740,18 @@ def test_one_token_right_behind_its_router_and_quantizer(ttq):
         out = ttq.moe_lowbit(xs[0], ids, w, layer.inv_s, layer.up,
                              layer.inv_s_mid, layer.down, 4, 32)
         assert torch.equal(out, want[0])
+
+
+@pytest.mark.parametrize("K,T", [(10000, 40), (11008, 8)])
+def test_adapters_fp32_over_a_long_input(ttq, K, T):
+    """fp32 stays fp32 over a long K: the error's 2-norm within 1e-6 of the
+    result's. Rounded additions of n random terms are off by about sqrt(n)
+    2^-24 of a term's size, 2^-24 of the sum's; sums that the tensor core cuts
+    are off by up to n / 16 times 2^-24 of it."""
+    a = make_adapters(T, 2, 16, K, 256, torch.float32)
+    a["Y"].zero_()
+    a["index"].fill_(1)
+    out = check_adapters(ttq, a)
+    ref = adapters_reference(a, a["scale"])[0]
+    err = ((out.double().cpu() - ref).norm() / ref.norm()).item()
+    assert err < 1e-6, err
