@@ -7,6 +7,12 @@
 // programmatic stream serialisation: up_kernel and down_kernel build their
 // lists from ids and fetch their first weights while the rows kernel before
 // them is still running.
+//
+// Measured by graph replay, bf16: 20 us for one token on 6 of 64 experts of
+// 2048 x 1408 (4 bits, groups of 128; 28 MB), 205 us for 33 tokens on 8 experts
+// of 4096 x 11008 (584 MB: 2.9 TB/s), 328 us for 64 tokens on 64 experts of
+// 4096 x 1408 (5 bits; 737 MB). The up kernel there issues 52-55 % of the
+// time with the ALU pipe 54-65 % busy: unpacking bounds it before HBM does.
 #include "moe.h"
 
 #include <algorithm>
